@@ -9,7 +9,9 @@ with ``python -m bit_block_quantized_q4_amd.build``).
 
 Functions mirror the C entry points: ``q4_packed_size``,
 ``q4_gemm_workspace_size``, ``q4_gemm_workspace_size_dt``, ``q4_quantize``, ``q4_gemv``, ``q4_gemm``,
-``q4_gemm_noalloc``, ``q4_status_string``, ``q4_abi_version``.
+``q4_gemm_noalloc``, ``q4_status_string``, ``q4_abi_version``; the fused linear
+layer ``q4_linear``; the experts' ``q4_route``, ``q4_route_plan``, ``q4_experts``
+and ``q4_moe``, with their size helpers.
 """
 
 from __future__ import annotations
@@ -42,6 +44,29 @@ Q4_F32 = 0
 Q4_F16 = 1
 Q4_BF16 = 2
 
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_erf": 3, "silu": 4}
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
+MAX_EXPERTS = 1024
+MAX_TOPK = 32
+
+
+class Epilogue(ctypes.Structure):
+    """q4_epilogue."""
+    _fields_ = [("bias", ctypes.c_void_p), ("bias_dtype", ctypes.c_int),
+                ("activation", ctypes.c_int), ("gated", ctypes.c_int),
+                ("residual", ctypes.c_void_p)]
+
+
+class Routing(ctypes.Structure):
+    """q4_routing."""
+    _fields_ = [("score", ctypes.c_int), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int),
+                ("group_topk", ctypes.c_int), ("group_score", ctypes.c_int),
+                ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+_P, _I, _L, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+
 # Every function the header declares, with (restype, argtypes).
 _SIGS = {
     "q4_abi_version": (ctypes.c_int, []),
@@ -61,6 +86,15 @@ _SIGS = {
     "q4_gemm_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
                                        ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                        ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]),
+    "q4_linear_workspace_size": (_Z, [_L, _L, _L, _I, _I]),
+    "q4_linear": (_I, [_P, _I, _P, _P, _P, _I, _L, _L, _L, _P, _Z, _P]),
+    "q4_route_plan_size": (_Z, [_L, _L, _L]),
+    "q4_route": (_I, [_P, _I, _L, _L, _L, _P, _P, _P, _P, _P]),
+    "q4_route_plan": (_I, [_P, _L, _L, _L, _P, _P]),
+    "q4_experts_workspace_size": (_Z, [_L] * 6 + [_I] * 3),
+    "q4_experts": (_I, [_P, _I, _L, _P, _P, _P, _P, _P, _I] + [_L] * 5 + [_P, _Z, _P]),
+    "q4_moe_workspace_size": (_Z, [_L] * 5 + [_I] * 2),
+    "q4_moe": (_I, [_P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I] + [_L] * 5 + [_P, _P, _P, _Z, _P]),
 }
 
 
@@ -271,4 +305,304 @@ def q4_gemm_noalloc(x, packed, y, stream=None, n=None, k=None):
     _check(lib().q4_gemm_noalloc(x.data_ptr(), _dtype_code(x), packed.data_ptr(), y.data_ptr(),
                                  _dtype_code(y), m, n, k, _stream_handle(stream, x.device)),
            "q4_gemm_noalloc")
+    return y
+
+
+# ------------------------------------------------------------ fused layers
+
+def _code(table, value, what):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{what} must be one of {', '.join(table)}; got {value!r}") from None
+
+
+def _same_device(x, **others):
+    _need_device(x, "x")
+    for name, t in others.items():
+        if t is not None:
+            _need_device(t, name)
+            if t.device != x.device:
+                raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+
+
+def _need_packed(packed, name="packed"):
+    if packed.dtype != _torch().uint8:
+        raise TypeError(f"{name} must be uint8; got {packed.dtype}")
+
+
+def _on(device):
+    """A context in which `device` is the current one (launches go there)."""
+    torch = _torch()
+    return torch.cuda.device(device)
+
+
+def _full_out(y, shape, dtype, device):
+    torch = _torch()
+    if y is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(y.shape) != tuple(shape):
+        raise ValueError(f"y must have shape {tuple(shape)}; got {tuple(y.shape)}")
+    return y
+
+
+def _out_dtype(y, y_dtype, x):
+    torch = _torch()
+    if y is not None:
+        return y.dtype
+    if y_dtype is None:
+        return x.dtype
+    if y_dtype in (Q4_BF16, torch.bfloat16, "bf16", "bfloat16"):
+        return torch.bfloat16
+    return _torch_dtype(y_dtype)
+
+
+def _epilogue(bias, activation, gated, residual, bias_shape, y):
+    if bias is not None and tuple(bias.shape) != tuple(bias_shape):
+        raise ValueError(f"bias must have shape {tuple(bias_shape)}; got {tuple(bias.shape)}")
+    if residual is not None and (residual.dtype != y.dtype or residual.shape != y.shape):
+        raise ValueError("residual must have y's shape and dtype "
+                         f"({tuple(y.shape)}, {y.dtype}); got {tuple(residual.shape)}, {residual.dtype}")
+    return Epilogue(None if bias is None else bias.data_ptr(),
+                    0 if bias is None else _dtype_code(bias), _code(ACTIVATIONS, activation, "activation"),
+                    1 if gated else 0, None if residual is None else residual.data_ptr())
+
+
+def _workspace(workspace, need, device):
+    """(tensor, pointer, bytes) of a workspace: the caller's, or one allocated here."""
+    torch = _torch()
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def q4_linear_workspace_size(m: int, n: int, k: int, x_dtype: int, gated: bool = False) -> int:
+    return lib().q4_linear_workspace_size(int(m), int(n), int(k), int(x_dtype), int(bool(gated)))
+
+
+def q4_linear(x, packed, bias=None, activation="none", gated=False, residual=None, y=None,
+              y_dtype=None, workspace=None, stream=None):
+    """Fused linear layer for any number of rows: z = x . dequant(packed)^T + bias,
+    then act(z), or with a gate act(z[:, :n/2]) * z[:, n/2:], plus the residual.
+
+    x [m, k] fp32, fp16 or bf16; packed [n, k/32*18] uint8; bias [n]; residual of
+    y's shape and dtype (it may be y itself).  activation: none, relu, gelu (tanh
+    form), gelu_erf or silu.  y defaults to x's dtype."""
+    _same_device(x, packed=packed, bias=bias, residual=residual, y=y, workspace=workspace)
+    _need_packed(packed)
+    n, k = packed_shape(packed)
+    if x.dim() != 2 or x.shape[1] != k:
+        raise ValueError(f"x must be [m, {k}]; got {tuple(x.shape)}")
+    m = int(x.shape[0])
+    y = _full_out(y, (m, n // 2 if gated else n), _out_dtype(y, y_dtype, x), x.device)
+    ep = _epilogue(bias, activation, gated, residual, (n,), y)
+    xd = _dtype_code(x)
+    L = lib()
+    workspace, wptr, wbytes = _workspace(
+        workspace, L.q4_linear_workspace_size(m, n, k, xd, ep.gated), x.device)
+    with _on(x.device):
+        _check(L.q4_linear(x.data_ptr(), xd, packed.data_ptr(), ctypes.byref(ep), y.data_ptr(),
+                           _dtype_code(y), m, n, k, wptr, wbytes, _stream_handle(stream, x.device)),
+               "q4_linear")
+    return y
+
+
+class Plan:
+    """The pairs (token, chosen expert) ordered by expert: what q4_route and
+    q4_route_plan return and q4_experts takes.
+
+    words: int32 device tensor; offsets [experts + 1] and order [m * topk] are
+    views of it (expert e's pairs i * topk + j are order[offsets[e]:offsets[e + 1]];
+    -1 behind the last pair that has an expert)."""
+
+    __slots__ = ("words", "m", "topk", "experts")
+
+    def __init__(self, words, m, topk, experts):
+        self.words, self.m, self.topk, self.experts = words, m, topk, experts
+
+    @property
+    def offsets(self):
+        return self.words[:self.experts + 1]
+
+    @property
+    def order(self):
+        at = (self.experts + 4) // 4 * 4
+        return self.words[at:at + self.m * self.topk]
+
+
+def q4_route_plan_size(m: int, topk: int, experts: int) -> int:
+    return lib().q4_route_plan_size(int(m), int(topk), int(experts))
+
+
+def _new_plan(m, topk, experts, device):
+    torch = _torch()
+    size = q4_route_plan_size(m, topk, experts)
+    if not size:
+        raise Q4Error(Q4_ERR_SHAPE, f"plan of {m} tokens, {topk} of {experts} experts")
+    return Plan(torch.empty(size // 4, dtype=torch.int32, device=device), m, topk, experts)
+
+
+def _routing(score, bias, groups, group_topk, group_score, renormalise, scale, experts):
+    torch = _torch()
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (experts,)):
+        raise ValueError(f"routing bias must be float32 [{experts}]; got {bias.dtype} {tuple(bias.shape)}")
+    return Routing(_code(SCORES, score, "score"), None if bias is None else bias.data_ptr(), int(groups),
+                   int(group_topk), _code(GROUP_SCORES, group_score, "group_score"),
+                   1 if renormalise else 0, float(scale))
+
+
+def _ids_out(t, shape, dtype, device, name):
+    torch = _torch()
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {shape}; got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def q4_route(logits, topk, score="softmax", bias=None, groups=1, group_topk=1, group_score="max",
+             renormalise=True, scale=1.0, ids=None, weights=None, stream=None):
+    """Choose topk experts per token from logits [m, experts] (fp32, fp16 or bf16).
+
+    score: softmax or sigmoid; bias [experts] fp32 is added for the choice only;
+    groups > 1 keeps the experts of the group_topk best groups (group_score: max,
+    or top2 for the sum of a group's two best).  Returns (ids [m, topk] int32,
+    weights [m, topk] fp32, plan); ties go to the lowest index, an expert with a
+    logit of -inf or NaN is not chosen, and a place without an expert is id -1,
+    weight 0."""
+    torch = _torch()
+    _same_device(logits, bias=bias, ids=ids, weights=weights)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [m, experts]; got {tuple(logits.shape)}")
+    m, experts, topk = int(logits.shape[0]), int(logits.shape[1]), int(topk)
+    r = _routing(score, bias, groups, group_topk, group_score, renormalise, scale, experts)
+    plan = _new_plan(m, topk, experts, logits.device)
+    ids = _ids_out(ids, (m, topk), torch.int32, logits.device, "ids")
+    weights = _ids_out(weights, (m, topk), torch.float32, logits.device, "weights")
+    with _on(logits.device):
+        _check(lib().q4_route(logits.data_ptr(), _dtype_code(logits), m, experts, topk, ctypes.byref(r),
+                              ids.data_ptr(), weights.data_ptr(), plan.words.data_ptr(),
+                              _stream_handle(stream, logits.device)), "q4_route")
+    return ids, weights, plan
+
+
+def q4_route_plan(ids, experts, stream=None):
+    """The plan of given ids [m, topk] int32; ids outside 0 .. experts - 1 name no expert."""
+    torch = _torch()
+    _need_device(ids, "ids")
+    if ids.dtype != torch.int32 or ids.dim() != 2:
+        raise ValueError(f"ids must be int32 [m, topk]; got {ids.dtype} {tuple(ids.shape)}")
+    m, topk = int(ids.shape[0]), int(ids.shape[1])
+    plan = _new_plan(m, topk, int(experts), ids.device)
+    with _on(ids.device):
+        _check(lib().q4_route_plan(ids.data_ptr(), m, topk, int(experts), plan.words.data_ptr(),
+                                   _stream_handle(stream, ids.device)), "q4_route_plan")
+    return plan
+
+
+def q4_experts_workspace_size(m: int, topk: int, experts: int, n: int, k: int, x_rows: int,
+                              x_dtype: int, gated: bool = False, combine: bool = False) -> int:
+    return lib().q4_experts_workspace_size(int(m), int(topk), int(experts), int(n), int(k), int(x_rows),
+                                           int(x_dtype), int(bool(gated)), int(bool(combine)))
+
+
+def _expert_shape(packed, what="packed"):
+    _need_packed(packed, what)
+    if packed.dim() != 3 or packed.shape[2] % BLOCK_BYTES:
+        raise ValueError(f"{what} must be [experts, n, k/32*18] uint8; got {tuple(packed.shape)}")
+    return int(packed.shape[0]), int(packed.shape[1]), int(packed.shape[2]) // BLOCK_BYTES * QK
+
+
+def q4_experts(x, packed, plan, bias=None, activation="none", gated=False, weights=None,
+               residual=None, y=None, y_dtype=None, workspace=None, stream=None):
+    """The chosen experts' products: row p = i * topk + j is
+    act(x_p . dequant(packed[e])^T + bias[e]) (gated as in q4_linear) for token i's
+    j-th expert e.
+
+    x: [m, k] (a token's row goes to all its experts) or [m * topk, k] (row p);
+    packed: [experts, n, k/32*18] uint8; bias: [experts, n].  Without `weights` y
+    is [m * topk, nout], and rows of pairs without an expert are left as they
+    were (not written); with weights [m, topk] fp32 y is [m, nout], the weighted
+    sum over a token's experts.  The residual has y's shape and dtype."""
+    torch = _torch()
+    _same_device(x, packed=packed, bias=bias, plan=plan.words, weights=weights, residual=residual, y=y,
+                 workspace=workspace)
+    experts, n, k = _expert_shape(packed)
+    m, topk = plan.m, plan.topk
+    if experts != plan.experts:
+        raise ValueError(f"packed has {experts} experts, the plan {plan.experts}")
+    if x.dim() != 2 or x.shape[1] != k or x.shape[0] not in (m, m * topk):
+        raise ValueError(f"x must be [{m} or {m * topk}, {k}]; got {tuple(x.shape)}")
+    if weights is not None and (weights.dtype != torch.float32 or tuple(weights.shape) != (m, topk)):
+        raise ValueError(f"weights must be float32 [{m}, {topk}]; got {weights.dtype} {tuple(weights.shape)}")
+    x_rows = int(x.shape[0])
+    y = _full_out(y, (m if weights is not None else m * topk, n // 2 if gated else n),
+                  _out_dtype(y, y_dtype, x), x.device)
+    ep = _epilogue(bias, activation, gated, residual, (experts, n), y)
+    xd = _dtype_code(x)
+    L = lib()
+    workspace, wptr, wbytes = _workspace(
+        workspace, L.q4_experts_workspace_size(m, topk, experts, n, k, x_rows, xd, ep.gated,
+                                               0 if weights is None else 1), x.device)
+    with _on(x.device):
+        _check(L.q4_experts(x.data_ptr(), xd, x_rows, packed.data_ptr(), ctypes.byref(ep),
+                            plan.words.data_ptr(), None if weights is None else weights.data_ptr(),
+                            y.data_ptr(), _dtype_code(y), m, topk, experts, n, k, wptr, wbytes,
+                            _stream_handle(stream, x.device)), "q4_experts")
+    return y
+
+
+def q4_moe_workspace_size(m: int, topk: int, experts: int, hidden: int, inter: int, x_dtype: int,
+                          gated: bool = True) -> int:
+    return lib().q4_moe_workspace_size(int(m), int(topk), int(experts), int(hidden), int(inter),
+                                       int(x_dtype), int(bool(gated)))
+
+
+def q4_moe(x, logits, up, down, topk, activation="silu", gated=True, up_bias=None, down_bias=None,
+           residual=None, score="softmax", route_bias=None, groups=1, group_topk=1, group_score="max",
+           renormalise=True, scale=1.0, ids=None, weights=None, y=None, y_dtype=None, workspace=None,
+           stream=None):
+    """A whole expert layer in one call: route the tokens by logits [m, experts], run
+    x [m, hidden] through the chosen experts' `up` ([experts, 2 * inter, ..] gated,
+    else [experts, inter, ..]; gate rows first) and `down` ([experts, hidden, ..]),
+    and add the rows up by the routing weights, plus the residual.  The rows between
+    the products have x's dtype.  Routing options as in q4_route; ids and weights
+    receive the routing if given."""
+    torch = _torch()
+    _same_device(x, logits=logits, up=up, down=down, up_bias=up_bias, down_bias=down_bias,
+                 residual=residual, route_bias=route_bias, ids=ids, weights=weights, y=y,
+                 workspace=workspace)
+    experts, nup, hidden = _expert_shape(up, "up")
+    e2, n2, inter = _expert_shape(down, "down")
+    if e2 != experts or n2 != hidden or nup != (2 * inter if gated else inter):
+        raise ValueError(f"up [{experts}, {nup}, k = {hidden}] and down [{e2}, {n2}, k = {inter}] do not match")
+    if x.dim() != 2 or x.shape[1] != hidden:
+        raise ValueError(f"x must be [m, {hidden}]; got {tuple(x.shape)}")
+    m, topk = int(x.shape[0]), int(topk)
+    if tuple(logits.shape) != (m, experts):
+        raise ValueError(f"logits must be [{m}, {experts}]; got {tuple(logits.shape)}")
+    r = _routing(score, route_bias, groups, group_topk, group_score, renormalise, scale, experts)
+    for t, dt, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
+        if t is not None:
+            _ids_out(t, (m, topk), dt, x.device, name)
+    y = _full_out(y, (m, hidden), _out_dtype(y, y_dtype, x), x.device)
+    if up_bias is not None and tuple(up_bias.shape) != (experts, nup):
+        raise ValueError(f"up_bias must have shape {(experts, nup)}; got {tuple(up_bias.shape)}")
+    up_ep = Epilogue(None if up_bias is None else up_bias.data_ptr(),
+                     0 if up_bias is None else _dtype_code(up_bias),
+                     _code(ACTIVATIONS, activation, "activation"), 1 if gated else 0, None)
+    down_ep = _epilogue(down_bias, "none", False, residual, (experts, hidden), y)
+    xd = _dtype_code(x)
+    L = lib()
+    workspace, wptr, wbytes = _workspace(
+        workspace, L.q4_moe_workspace_size(m, topk, experts, hidden, inter, xd, up_ep.gated), x.device)
+    with _on(x.device):
+        _check(L.q4_moe(x.data_ptr(), xd, logits.data_ptr(), _dtype_code(logits), ctypes.byref(r),
+                        up.data_ptr(), ctypes.byref(up_ep), down.data_ptr(), ctypes.byref(down_ep),
+                        y.data_ptr(), _dtype_code(y), m, topk, experts, hidden, inter,
+                        None if ids is None else ids.data_ptr(),
+                        None if weights is None else weights.data_ptr(), wptr, wbytes,
+                        _stream_handle(stream, x.device)), "q4_moe")
     return y

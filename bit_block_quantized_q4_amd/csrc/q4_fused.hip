@@ -1,0 +1,196 @@
+// The fused linear layer and the expert products: launch rules, and the
+// kernels that are right for every shape and type.
+//
+//   z[i, r] = sum_j x[i, j] (q[r, j] - 8) d[r, j / 32]
+//   y = act(z + b) (x the gated half) + residual
+//
+// fused_row_kernel: one wavefront per output column and up to eight rows of
+// x; a lane takes every 64th Q4_0 block of the column's weight row (of both
+// rows with a gate), sums x (q - 8) in fp32 and applies d per block, and the
+// wave adds its lanes' sums by xor shuffles, a fixed order.
+#include "q4_fused.hpp"
+
+namespace q4 {
+namespace {
+
+constexpr int kRowMT = 8;
+
+template <typename XT>
+__device__ __forceinline__ float widen(const XT* x, int64_t i);
+template <>
+__device__ __forceinline__ float widen<float>(const float* x, int64_t i) { return x[i]; }
+template <>
+__device__ __forceinline__ float widen<half_t>(const half_t* x, int64_t i) {
+  return static_cast<float>(x[i]);
+}
+template <>
+__device__ __forceinline__ float widen<bf16_t>(const bf16_t* x, int64_t i) {
+  return bf16_bits_to_float(x[i].bits);
+}
+
+// The 32 exact q - 8 of a block at p (2-byte aligned) and its scale.
+__device__ __forceinline__ float block_codes(const uint8_t* blk, float (&w)[kQK]) {
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(blk);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t c = p[1 + i];
+    w[2 * i] = static_cast<float>(static_cast<int>(c & 0xFu) - 8);
+    w[2 * i + 16] = static_cast<float>(static_cast<int>((c >> 4) & 0xFu) - 8);
+    w[2 * i + 1] = static_cast<float>(static_cast<int>((c >> 8) & 0xFu) - 8);
+    w[2 * i + 17] = static_cast<float>(static_cast<int>((c >> 12) & 0xFu) - 8);
+  }
+  return half_bits_to_float(p[0]);
+}
+
+// Workgroup = four output columns of one tile of rows (dense: all m rows).
+template <typename XT, int G>
+__global__ __launch_bounds__(256) void fused_row_kernel(const XT* __restrict__ x,
+                                                        const uint8_t* __restrict__ W, int64_t m,
+                                                        int64_t nout, int64_t k, int64_t cblocks,
+                                                        Epi ep, Rows rows) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t t = blockIdx.x / cblocks;
+  const int64_t c = (blockIdx.x - t * cblocks) * 4 + threadIdx.x / kWave;
+  if (c >= nout) return;  // whole wavefront
+  int64_t start = 0, count = m, boff = 0;
+  if (rows.order != nullptr) {
+    if (t >= *rows.ntiles) return;
+    const int4 tile = rows.tiles[t];
+    start = tile.y;
+    count = tile.z;
+    W += tile.x * rows.wstride;
+    boff = tile.x * rows.nbias;
+  }
+  const int64_t nb = k / kQK, rb = nb * kBlockBytes;
+  const uint8_t* wr[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) wr[g] = W + (c + g * ep.half) * rb;
+  for (int64_t r0 = 0; r0 < count; r0 += kRowMT) {
+    const int mt = static_cast<int>(count - r0 < kRowMT ? count - r0 : kRowMT);
+    const XT* xr[kRowMT];
+    int64_t yrow[kRowMT];
+#pragma unroll
+    for (int i = 0; i < kRowMT; ++i) {
+      const int64_t at = start + r0 + (i < mt ? i : mt - 1);  // rows past the last repeat it
+      const int64_t p = rows.order != nullptr ? rows.order[at] : at;
+      yrow[i] = p;
+      xr[i] = x + (rows.order != nullptr ? p / rows.xdiv : p) * k;
+    }
+    float acc[G][kRowMT];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < kRowMT; ++i) acc[g][i] = 0.f;
+    for (int64_t b = lane; b < nb; b += kWave) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float w[kQK];
+        const float d = block_codes(wr[g] + b * kBlockBytes, w);
+#pragma unroll
+        for (int i = 0; i < kRowMT; ++i) {
+          if (i < mt) {
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < kQK; ++j) s = fmaf(widen<XT>(xr[i], b * kQK + j), w[j], s);
+            acc[g][i] = fmaf(d, s, acc[g][i]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < kRowMT; ++i)
+#pragma unroll
+        for (int off = kWave / 2; off > 0; off >>= 1) acc[g][i] += __shfl_xor(acc[g][i], off);
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < kRowMT; ++i)
+        if (i < mt) finish_store(ep, boff, yrow[i], c, acc[0][i], acc[G - 1][i]);
+    }
+  }
+}
+
+// y[i] = sum_j weights[i, j] rows[i topk + j] + residual[i] in the order of j;
+// a pair whose pos is negative has no expert and counts 0.  One column per
+// thread.
+__global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part,
+                                                      const float* __restrict__ weights,
+                                                      const int* __restrict__ pos, int64_t m,
+                                                      int topk, int64_t nout, Epi ep) {
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= m * nout) return;
+  const int64_t i = at / nout, c = at - i * nout;
+  float v = 0.f;
+  for (int j = 0; j < topk; ++j) {
+    const int64_t p = i * topk + j;
+    if (pos[p] >= 0) v = fmaf(weights[p], part[p * nout + c], v);
+  }
+  if (ep.residual != nullptr) v += load_f32(ep.residual, ep.y_dt, at);
+  store_as(ep.y, ep.y_dt, at, v);
+}
+
+Rows plan_rows(const Product& p) {
+  Rows r;
+  if (p.experts == 0) return r;
+  const PlanLayout L = plan_layout(p.m, p.topk, p.experts);
+  r.order = p.plan + L.order;
+  r.ntiles = p.plan + L.head;
+  r.tiles = reinterpret_cast<const int4*>(p.plan + L.tiles);
+  r.xdiv = p.x_rows == p.m ? static_cast<int>(p.topk) : 1;
+  r.wstride = p.n * (p.k / kQK) * kBlockBytes;
+  r.nbias = p.n;
+  return r;
+}
+
+template <typename XT>
+hipError_t launch_row(const Product& p, const Epi& ep0, hipStream_t s) {
+  Epi ep = ep0;
+  Rows rows = plan_rows(p);
+  const XT* x = static_cast<const XT*>(p.x);
+  const uint8_t* W = p.W;
+  int64_t m = p.m, nout = ep.ldy, k = p.k, cblocks = (nout + 3) / 4;
+  const int64_t tiles = p.experts == 0 ? 1 : plan_layout(p.m, p.topk, p.experts).max_tiles;
+  void* argv[] = {&x, &W, &m, &nout, &k, &cblocks, &ep, &rows};
+  const void* fn = ep.half != 0 ? reinterpret_cast<const void*>(&fused_row_kernel<XT, 2>)
+                                : reinterpret_cast<const void*>(&fused_row_kernel<XT, 1>);
+  return hipLaunchKernel(fn, dim3(static_cast<unsigned>(cblocks * tiles)), dim3(256), argv, 0, s);
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t product_workspace_bytes(int64_t m, int64_t topk, int64_t experts, int64_t n, int64_t k,
+                               int64_t x_rows, DType xt, bool gated, bool combine) {
+  (void)k; (void)x_rows; (void)xt; (void)experts;
+  size_t b = 0;
+  if (combine) b += up256(static_cast<size_t>(m * topk) * static_cast<size_t>(gated ? n / 2 : n) * 4);
+  return b;
+}
+
+hipError_t launch_product(const Product& p, void* workspace, hipStream_t s) {
+  Epi ep = p.ep;
+  if (p.weights != nullptr) {  // fp32 rows first, then their sums
+    ep.y = workspace;
+    ep.y_dt = static_cast<int>(DType::F32);
+    ep.residual = nullptr;
+  }
+  hipError_t e;
+  if (p.xt == DType::F32) e = launch_row<float>(p, ep, s);
+  else if (p.xt == DType::F16) e = launch_row<half_t>(p, ep, s);
+  else e = launch_row<bf16_t>(p, ep, s);
+  if (e != hipSuccess || p.weights == nullptr) return e;
+  const PlanLayout L = plan_layout(p.m, p.topk, p.experts);
+  const float* part = static_cast<const float*>(workspace);
+  const float* w = p.weights;
+  const int* pos = p.plan + L.pos;
+  int64_t m = p.m, nout = ep.ldy;
+  int topk = static_cast<int>(p.topk);
+  Epi out = p.ep;
+  void* argv[] = {&part, &w, &pos, &m, &topk, &nout, &out};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&combine_kernel),
+                         dim3(static_cast<unsigned>((m * nout + 255) / 256)), dim3(256), argv, 0, s);
+}
+
+}  // namespace q4

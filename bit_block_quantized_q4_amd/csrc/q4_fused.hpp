@@ -1,0 +1,158 @@
+// Shared by the fused linear layer, the expert products and the routing
+// (gfx950).  Internal header.
+#pragma once
+
+#include "q4_device.hpp"
+
+namespace q4 {
+
+enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluErf = 3, kActSilu = 4 };
+
+// What follows a product, and where its outputs go (see q4_epilogue in the
+// public header).  Passed to kernels by value.
+struct Epi {
+  const void* bias = nullptr;  // [n], or [experts][n]
+  const void* residual = nullptr;
+  void* y = nullptr;
+  int64_t ldy = 0;   // output columns
+  int64_t half = 0;  // gated: the "up" row of output column c is weight row half + c; 0: no gate
+  int bias_dt = 0, act = 0, y_dt = 0;
+};
+
+// Which rows of x a product takes.  order == nullptr: one group, rows 0 ..
+// m - 1 of x and y.  Otherwise tile t of the plan covers the pairs
+// order[start .. start + count - 1] of one expert; pair p reads row p / xdiv
+// of x and writes row p of y.
+struct Rows {
+  const int* order = nullptr;
+  const int* ntiles = nullptr;  // tiles in use (the grid is an upper bound)
+  const int4* tiles = nullptr;  // {expert, start, count, 0}
+  int xdiv = 1;
+  int64_t wstride = 0;  // packed bytes per expert
+  int64_t nbias = 0;    // bias values per expert
+};
+
+// ------------------------------------------------------------------ plan
+//
+// Device layout of a plan in int32 words: offsets[experts + 1], order[pairs],
+// pos[pairs] (the place of a pair in `order`, -1 without an expert), {ntiles,
+// rows per tile, 0, 0}, tiles of four words.  Every part starts at a multiple
+// of four words.
+struct PlanLayout {
+  int64_t order, pos, head, tiles, words;
+  int64_t max_tiles;
+  int tile_rows;
+};
+
+// Rows per tile of the expert products, by the mean number of rows per
+// expert alone, so that one plan serves every product over it: 16 (one
+// activation tile of the matrix-core decode kernel) up to 12 rows, 32 up to
+// 40, then the 128-row tiles of the prefill kernel.
+inline int expert_tile_rows(int64_t m, int64_t topk, int64_t experts) {
+  const double mean = static_cast<double>(m) * static_cast<double>(topk) / static_cast<double>(experts);
+  return mean <= 12.0 || m <= 16 ? 16 : mean <= 40.0 || m <= 32 ? 32 : 128;
+}
+
+inline PlanLayout plan_layout(int64_t m, int64_t topk, int64_t experts) {
+  PlanLayout p;
+  const int64_t pairs = m * topk;
+  auto up4 = [](int64_t v) { return (v + 3) / 4 * 4; };
+  p.tile_rows = expert_tile_rows(m, topk, experts);
+  // whole tiles, plus one partial tile for every expert that has rows
+  p.max_tiles = pairs / p.tile_rows + (pairs < experts ? pairs : experts);
+  p.order = up4(experts + 1);
+  p.pos = p.order + up4(pairs);
+  p.head = p.pos + up4(pairs);
+  p.tiles = p.head + 4;
+  p.words = p.tiles + 4 * p.max_tiles;
+  return p;
+}
+
+// ------------------------------------------------------------------ values
+
+// Element i of a dtype-coded array, as fp32 (exact).
+__device__ __forceinline__ float load_f32(const void* p, int dt, int64_t i) {
+  if (dt == static_cast<int>(DType::F32)) return static_cast<const float*>(p)[i];
+  const uint16_t b = static_cast<const uint16_t*>(p)[i];
+  return dt == static_cast<int>(DType::F16) ? half_bits_to_float(b) : bf16_bits_to_float(b);
+}
+
+// fp32 -> 16 bits, to nearest even.
+__device__ __forceinline__ uint16_t f32_to_16(float v, int dt) {
+  if (dt == static_cast<int>(DType::F16)) return __builtin_bit_cast(uint16_t, static_cast<half_t>(v));
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+
+__device__ __forceinline__ void store_as(void* p, int dt, int64_t i, float v) {
+  if (dt == static_cast<int>(DType::F32)) static_cast<float*>(p)[i] = v;
+  else static_cast<uint16_t*>(p)[i] = f32_to_16(v, dt);
+}
+
+// silu and the tanh form of gelu as z / (1 + exp(-t)): no cancellation for
+// negative z, and 0 (not NaN) where exp overflows.
+__device__ __forceinline__ float activate(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.f || z != z ? z : 0.f;
+    case kActSilu: return z / (1.f + expf(-z));
+    case kActGelu: return z / (1.f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+    case kActGeluErf: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    default: return z;
+  }
+}
+
+// Output column c of one row from its weight row sums (z1: the "up" row's,
+// read with a gate only), without the residual.  e: expert (0 without).
+__device__ __forceinline__ float finish(const Epi& ep, int64_t boff, int64_t c, float z0, float z1) {
+  if (ep.bias != nullptr) {
+    z0 += load_f32(ep.bias, ep.bias_dt, boff + c);
+    if (ep.half != 0) z1 += load_f32(ep.bias, ep.bias_dt, boff + ep.half + c);
+  }
+  const float a = activate(z0, ep.act);
+  return ep.half != 0 ? a * z1 : a;
+}
+
+// As finish, with the residual, stored to row `row` of y.
+__device__ __forceinline__ void finish_store(const Epi& ep, int64_t boff, int64_t row, int64_t c,
+                                             float z0, float z1) {
+  float v = finish(ep, boff, c, z0, z1);
+  const int64_t at = row * ep.ldy + c;
+  if (ep.residual != nullptr) v += load_f32(ep.residual, ep.y_dt, at);
+  store_as(ep.y, ep.y_dt, at, v);
+}
+
+// ------------------------------------------------------------------ launchers
+
+// A product as the launchers take it.
+struct Product {
+  const void* x;
+  DType xt;
+  int64_t x_rows;
+  const uint8_t* W;
+  int64_t m;  // rows of one group (dense), or tokens
+  int64_t n, k;
+  int64_t topk = 1, experts = 0;  // experts == 0: dense
+  const int* plan = nullptr;      // experts: the plan's words
+  const float* weights = nullptr; // experts, combined
+  Epi ep;
+};
+
+size_t product_workspace_bytes(int64_t m, int64_t topk, int64_t experts, int64_t n, int64_t k,
+                               int64_t x_rows, DType xt, bool gated, bool combine);
+hipError_t launch_product(const Product& p, void* workspace, hipStream_t s);
+
+struct RouteArgs {
+  const void* logits;
+  DType dt;
+  int64_t m, experts, topk;
+  const float* bias;
+  int sigmoid, groups, group_topk, top2, renormalise;
+  float scale;
+  int* ids;
+  float* weights;
+  int* plan;  // may be null
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+hipError_t launch_route_plan(const int* ids, int64_t m, int64_t topk, int64_t experts, int* plan,
+                             hipStream_t s);
+
+}  // namespace q4

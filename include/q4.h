@@ -88,7 +88,8 @@ typedef enum q4_dtype {
   Q4_F32 = 0, /* IEEE binary32 */
   Q4_F16 = 1, /* IEEE binary16 */
   Q4_BF16 = 2 /* bfloat16: the upper 16 bits of a binary32 pattern; accepted
-                 for weights and activations, not for outputs */
+                 for weights and activations, not for the outputs of q4_gemv
+                 and q4_gemm */
 } q4_dtype;
 
 /* Version of this ABI (Q4_ABI_VERSION). */
@@ -177,6 +178,162 @@ q4_status q4_gemm(const void *x, int x_dtype, const void *packed, void *y,
 q4_status q4_gemm_noalloc(const void *x, int x_dtype, const void *packed, void *y,
                           int y_dtype, int64_t m, int64_t n, int64_t k,
                           q4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Fused linear layer
+ * ------------------------------------------------------------------------
+ * The calls below also write Q4_BF16 outputs and take any m >= 1 (one entry
+ * for decode and prefill).  Conventions are those at the top of this header
+ * except where stated. */
+
+typedef enum q4_activation {
+  Q4_ACT_NONE = 0,
+  Q4_ACT_RELU = 1,     /* max(z, 0) */
+  Q4_ACT_GELU = 2,     /* z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+  Q4_ACT_GELU_ERF = 3, /* z / 2 (1 + erf(z / sqrt(2))) */
+  Q4_ACT_SILU = 4      /* z / (1 + exp(-z)) */
+} q4_activation;
+
+/* What follows a product z = x . dequant(packed)^T of n weight rows:
+ *   z += bias                             (n values of bias_dtype; NULL: none)
+ *   gated == 0:  v = act(z)               n output columns
+ *   gated != 0:  v = act(z[:n/2]) z[n/2:] n / 2 output columns (n even): the
+ *                first half of the weight rows is the gate, the second the
+ *                factor ("up") rows
+ *   y = v + residual                      (shape and dtype of y; NULL: none)
+ * all in fp32 with one rounding to y.  residual may be y itself (the same
+ * pointer: accumulation in place) but not overlap it otherwise.  bias and
+ * residual are 16-byte aligned. */
+typedef struct q4_epilogue {
+  const void *bias;
+  int bias_dtype;  /* q4_dtype; read only with a bias */
+  int activation;  /* q4_activation */
+  int gated;       /* 0 or 1 */
+  const void *residual;
+} q4_epilogue;
+
+/* Bytes of workspace q4_linear needs (0 when none, or for an invalid shape
+ * or dtype). */
+size_t q4_linear_workspace_size(int64_t m, int64_t n, int64_t k, int x_dtype, int gated);
+
+/* Fused linear layer: y = epilogue(x[m][k] . dequant(packed[n])^T) for any
+ * m >= 1; y is [m][n], or [m][n / 2] with a gate, of any q4_dtype.
+ * `epilogue` may be NULL (the plain product).
+ *   - fp32 x: fp32 products of the exactly decoded weights.
+ *   - fp16 and bf16 x on matrix cores: for m <= 32 the weight codes enter as
+ *     exact integers and the block scales in fp32, as in q4_gemv; above, the
+ *     weights are dequantised to fp16 (one rounding, 2^-11 relative) as in
+ *     q4_gemm, with the exact route for tiles where that overflows.
+ *   - bf16 x may be staged as fp16, every row multiplied by the power of two
+ *     that brings its largest magnitude to [2^15, 2^16): exact for every
+ *     value of at least 2^-32 of that magnitude; a smaller one is rounded to
+ *     a multiple of 2^-39 of it.
+ * `workspace` holds q4_linear_workspace_size bytes (NULL when that is 0),
+ * overlaps no other buffer and is shared by no call that may run at the same
+ * time (calls on several streams, graphs replayed at once). */
+q4_status q4_linear(const void *x, int x_dtype, const void *packed,
+                    const q4_epilogue *epilogue, void *y, int y_dtype, int64_t m,
+                    int64_t n, int64_t k, void *workspace, size_t workspace_bytes,
+                    q4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Experts
+ * ------------------------------------------------------------------------ */
+
+#define Q4_MAX_EXPERTS 1024
+#define Q4_MAX_TOPK 32
+
+typedef enum q4_score { Q4_SCORE_SOFTMAX = 0, Q4_SCORE_SIGMOID = 1 } q4_score;
+typedef enum q4_group_score {
+  Q4_GROUP_MAX = 0, /* a group counts as its best expert */
+  Q4_GROUP_TOP2 = 1 /* a group counts as the sum of its two best experts */
+} q4_group_score;
+
+/* How experts are chosen.  For a token with logits l[experts]:
+ *   s    = softmax(l) or sigmoid(l), element by element
+ *   key  = s + bias; without a bias and with Q4_GROUP_MAX the logit itself
+ *          (the same order)
+ *   groups > 1: the experts are `groups` consecutive groups of equal size;
+ *          only those in the group_topk best groups remain
+ *   the topk largest keys are chosen, in descending order
+ *   weight = s of the chosen (without bias); with renormalise divided by the
+ *          sum over the chosen (0 if that sum is 0); times scale
+ * Keys are formed and compared in 64 bits; ties go to the lowest index
+ * (experts and groups alike).  An expert whose logit is -infinity or NaN, or
+ * whose bias is -infinity or NaN, is never chosen for that token and counts 0
+ * in a group's sum; where fewer than topk experts remain the rest of the row
+ * is id -1, weight 0.  +infinity counts as the largest finite fp32. */
+typedef struct q4_routing {
+  int score;         /* q4_score */
+  const float *bias; /* [experts] fp32 device array, 4-byte aligned; NULL: none */
+  int groups;        /* >= 1, divides experts */
+  int group_topk;    /* 1 .. groups */
+  int group_score;   /* q4_group_score; read when groups > 1 */
+  int renormalise;   /* 0 or 1 */
+  float scale;       /* finite */
+} q4_routing;
+
+/* Bytes of a plan for m tokens with topk of `experts` experts each: int32
+ * words, first offsets[experts + 1] (expert e's pairs are order[offsets[e]] ..
+ * order[offsets[e + 1] - 1]; padded to a multiple of 4 words), then
+ * order[m topk]: the pair numbers i topk + j, by expert and ascending within
+ * one, then -1 for pairs whose id names no expert.  What follows is the
+ * library's own.  0 for an invalid shape. */
+size_t q4_route_plan_size(int64_t m, int64_t topk, int64_t experts);
+
+/* Routing: ids[m][topk] (int32), weights[m][topk] (fp32) and, unless NULL, a
+ * plan of q4_route_plan_size bytes from logits[m][experts] (Q4_F32, Q4_F16 or
+ * Q4_BF16). */
+q4_status q4_route(const void *logits, int logits_dtype, int64_t m, int64_t experts,
+                   int64_t topk, const q4_routing *routing, int32_t *ids, float *weights,
+                   void *plan, q4_stream_t stream);
+
+/* The plan of given ids[m][topk]; an id outside 0 .. experts - 1 names no
+ * expert.  A token may name the same expert more than once. */
+q4_status q4_route_plan(const int32_t *ids, int64_t m, int64_t topk, int64_t experts,
+                        void *plan, q4_stream_t stream);
+
+/* Bytes of workspace q4_experts needs (0 when none or for an invalid shape).
+ * `x_rows` and `combine` as below. */
+size_t q4_experts_workspace_size(int64_t m, int64_t topk, int64_t experts, int64_t n, int64_t k,
+                                 int64_t x_rows, int x_dtype, int gated, int combine);
+
+/* The products of the chosen experts.  packed is [experts][n][k] Q4_0 (each
+ * expert's rows as in q4_packed_size, experts contiguous), the epilogue's bias
+ * [experts][n].  Pair p = i topk + j is token i's j-th expert e:
+ *   row p = act((x_p . dequant(packed[e])^T) + bias[e])   (gated: as above)
+ * with x_p = x[i] for x_rows == m and x_p = x[p] for x_rows == m topk.
+ *   weights == NULL: y is [m topk][nout], y[p] = row p + residual[p]; a pair
+ *     without an expert leaves its row of y as it was.
+ *   weights != NULL (fp32 [m][topk]): y is [m][nout],
+ *     y[i] = sum_j weights[i][j] row(i topk + j) + residual[i], summed in fp32
+ *     in the order of j; pairs without an expert count 0.
+ * `plan` is what q4_route or q4_route_plan wrote for the same m, topk and
+ * experts.  Types, routes and the workspace are q4_linear's; which route runs
+ * goes by the mean number of rows per expert. */
+q4_status q4_experts(const void *x, int x_dtype, int64_t x_rows, const void *packed,
+                     const q4_epilogue *epilogue, const void *plan, const float *weights,
+                     void *y, int y_dtype, int64_t m, int64_t topk, int64_t experts,
+                     int64_t n, int64_t k, void *workspace, size_t workspace_bytes,
+                     q4_stream_t stream);
+
+/* Bytes of workspace q4_moe needs (0 for an invalid shape). */
+size_t q4_moe_workspace_size(int64_t m, int64_t topk, int64_t experts, int64_t hidden,
+                             int64_t inter, int x_dtype, int gated);
+
+/* A whole expert layer: q4_route on logits[m][experts], q4_experts on x[m][hidden]
+ * with `up` ([experts][inter or, gated, 2 inter][hidden]) into rows of x's dtype,
+ * and q4_experts on those with `down` ([experts][hidden][inter]), combined by the
+ * routing weights into y[m][hidden].  up_epilogue carries the activation, the
+ * gate and [experts][..] bias (no residual); down_epilogue (may be NULL) the
+ * bias and the residual (no activation, no gate).  ids and weights receive the
+ * routing unless NULL. */
+q4_status q4_moe(const void *x, int x_dtype, const void *logits, int logits_dtype,
+                 const q4_routing *routing, const void *up, const q4_epilogue *up_epilogue,
+                 const void *down, const q4_epilogue *down_epilogue, void *y, int y_dtype,
+                 int64_t m, int64_t topk, int64_t experts, int64_t hidden, int64_t inter,
+                 int32_t *ids, float *weights, void *workspace, size_t workspace_bytes,
+                 q4_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,74 @@
+"""The fused linear layer and the experts against 64-bit forms, at the sizes,
+types and masks where they can go wrong."""
+
+import numpy as np
+import pytest
+import torch
+
+from _fused import (TYPES, check, experts64, finish64, plan64, product64, route64, rows, weights)
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(t, gpu):
+    return None if t is None else t.to(gpu)
+
+
+def run_linear(q4lib, gpu, m, n, k, xt, yt=None, act="none", gated=False, bias=None, residual=False,
+               inplace=False, seed=0, scale=1.0):
+    yt = yt or xt
+    packed, w = weights(seed + 1, n, k)
+    x = rows(seed + 2, xt, m, k, scale=scale)
+    nout = n // 2 if gated else n
+    b = rows(seed + 3, bias, n, scale=0.3) if bias else None
+    r = rows(seed + 4, yt, m, nout) if residual else None
+    kw = {}
+    if inplace:
+        kw["y"] = kw["residual"] = dev(r, gpu).clone()
+    else:
+        kw["residual"] = dev(r, gpu)
+    y = q4lib.q4_linear(dev(x, gpu), dev(packed, gpu), bias=dev(b, gpu), activation=act, gated=gated,
+                        y_dtype=TYPES[yt], **kw)
+    assert y.dtype == TYPES[yt]
+    v, err = product64(x, w, b, act, gated, rounded=m > 32 and xt != "f32", scaled=xt == "bf16")
+    v, err = finish64(v, err, r, TYPES[yt])
+    check(y, v, err, f"m{m} n{n} k{k} {xt}->{yt} {act} gated={gated}")
+    return y
+
+
+SIZES = [(1, 1, 32), (1, 7, 96), (1, 512, 512), (2, 66, 64), (3, 130, 128), (5, 34, 1056), (8, 96, 256),
+         (10, 516, 512), (16, 260, 1408), (17, 200, 1024), (31, 1028, 512), (32, 70, 704), (33, 130, 512),
+         (40, 258, 96), (64, 96, 544), (127, 300, 1024), (128, 128, 256), (257, 516, 1088), (300, 260, 2048)]
+
+
+@pytest.mark.parametrize("xt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_linear_plain_sizes(q4lib, gpu, m, n, k, xt):
+    run_linear(q4lib, gpu, m, n, k, xt, seed=m + n + k)
+
+
+@pytest.mark.parametrize("xt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(m, n + n % 2, k) for m, n, k in SIZES])
+def test_linear_gated_sizes(q4lib, gpu, m, n, k, xt):
+    run_linear(q4lib, gpu, m, n, k, xt, act="silu", gated=True, bias=xt, residual=True, seed=m + n + k + 7)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_erf", "silu"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("m", [1, 6, 20, 150])
+def test_linear_activations(q4lib, gpu, m, act, gated):
+    run_linear(q4lib, gpu, m, 136, 512, "f16", act=act, gated=gated, bias="f16", seed=m, scale=3.0)
+
+
+@pytest.mark.parametrize("xt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("yt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("bt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("m", [2, 70])
+def test_linear_types(q4lib, gpu, m, xt, yt, bt):
+    run_linear(q4lib, gpu, m, 96, 256, xt, yt, act="gelu", bias=bt, residual=True, seed=11)
+
+
+@pytest.mark.parametrize("m", [1, 12, 32, 64, 200])
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_in_place_residual(q4lib, gpu, m, gated):
+    run_linear(q4lib, gpu, m, 264, 512, "bf16", act="silu", gated=gated, residual=True, inplace=True, seed=m)
