@@ -14,6 +14,7 @@ namespace q4 {
 namespace {
 
 constexpr int kRowMT = 8;
+constexpr int kFewRows = 32;  // most rows per product of the decode kernels
 
 template <typename XT>
 __device__ __forceinline__ float widen(const XT* x, int64_t i);
@@ -161,28 +162,52 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
+// Rows of a product from which it runs on the prefill tiles.
+bool many_rows(int64_t m, int64_t topk, int64_t experts) {
+  return experts == 0 ? m > kFewRows : expert_tile_rows(m, topk, experts) > kFewRows;
+}
+
 size_t product_workspace_bytes(int64_t m, int64_t topk, int64_t experts, int64_t n, int64_t k,
                                int64_t x_rows, DType xt, bool gated, bool combine) {
-  (void)k; (void)x_rows; (void)xt; (void)experts;
   size_t b = 0;
+  if (many_rows(m, topk, experts)) {
+    if (xt == DType::BF16) b += stage_bytes(x_rows, k);
+    b += fused_gemm_bytes(m, n, k, xt, gated, experts != 0);
+  }
   if (combine) b += up256(static_cast<size_t>(m * topk) * static_cast<size_t>(gated ? n / 2 : n) * 4);
   return b;
 }
 
 hipError_t launch_product(const Product& p, void* workspace, hipStream_t s) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   Epi ep = p.ep;
+  const float* part = reinterpret_cast<const float*>(ws);
   if (p.weights != nullptr) {  // fp32 rows first, then their sums
-    ep.y = workspace;
+    ep.y = ws;
     ep.y_dt = static_cast<int>(DType::F32);
     ep.residual = nullptr;
+    ws += up256(static_cast<size_t>(p.m * p.topk) * static_cast<size_t>(ep.ldy) * 4);
   }
-  hipError_t e;
-  if (p.xt == DType::F32) e = launch_row<float>(p, ep, s);
-  else if (p.xt == DType::F16) e = launch_row<half_t>(p, ep, s);
-  else e = launch_row<bf16_t>(p, ep, s);
+  hipError_t e = hipSuccess;
+  if (many_rows(p.m, p.topk, p.experts)) {
+    const half_t* xs = static_cast<const half_t*>(p.x);
+    const float* scale = nullptr;
+    if (p.xt == DType::BF16) {
+      e = launch_stage(p.x, p.x_rows, p.k, ws, &xs, &scale, s);
+      if (e != hipSuccess) return e;
+      ws += stage_bytes(p.x_rows, p.k);
+    }
+    const int64_t tiles = p.experts == 0 ? 0 : plan_layout(p.m, p.topk, p.experts).max_tiles;
+    e = launch_fused_gemm(p, ep, plan_rows(p), xs, scale, tiles, ws, s);
+  } else if (p.xt == DType::F32) {
+    e = launch_row<float>(p, ep, s);
+  } else if (p.xt == DType::F16) {
+    e = launch_row<half_t>(p, ep, s);
+  } else {
+    e = launch_row<bf16_t>(p, ep, s);
+  }
   if (e != hipSuccess || p.weights == nullptr) return e;
   const PlanLayout L = plan_layout(p.m, p.topk, p.experts);
-  const float* part = static_cast<const float*>(workspace);
   const float* w = p.weights;
   const int* pos = p.plan + L.pos;
   int64_t m = p.m, nout = ep.ldy;

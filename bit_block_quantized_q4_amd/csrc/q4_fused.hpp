@@ -140,6 +140,14 @@ size_t product_workspace_bytes(int64_t m, int64_t topk, int64_t experts, int64_t
                                int64_t x_rows, DType xt, bool gated, bool combine);
 hipError_t launch_product(const Product& p, void* workspace, hipStream_t s);
 
+// Matrix-core products of many rows (16-bit x, and fp32 x on the exact route).
+size_t stage_bytes(int64_t rows, int64_t k);
+hipError_t launch_stage(const void* x, int64_t rows, int64_t k, void* ws, const half_t** xs,
+                        const float** scale, hipStream_t s);
+size_t fused_gemm_bytes(int64_t m, int64_t n, int64_t k, DType xt, bool gated, bool grouped);
+hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
+                             const float* xscale, int64_t row_tiles, void* workspace, hipStream_t s);
+
 struct RouteArgs {
   const void* logits;
   DType dt;

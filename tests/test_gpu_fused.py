@@ -72,3 +72,46 @@ def test_linear_types(q4lib, gpu, m, xt, yt, bt):
 @pytest.mark.parametrize("gated", [False, True])
 def test_linear_in_place_residual(q4lib, gpu, m, gated):
     run_linear(q4lib, gpu, m, 264, 512, "bf16", act="silu", gated=gated, residual=True, inplace=True, seed=m)
+
+
+@pytest.mark.parametrize("xt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(3, 70, 512), (70, 200, 96), (150, 300, 512), (300, 516, 1024), (1030, 260, 320)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_scales_beyond_fp16(q4lib, gpu, m, n, k, xt, gated):
+    """Block scales whose largest weight is beyond fp16 (80000): only some tiles
+    meet them, and the residual is y itself, which those must find unchanged."""
+    import oracle
+    from _fused import decode
+    rng = np.random.default_rng(m)
+    w = (rng.standard_normal((n, k)) * 0.05).astype(np.float32)
+    w[n // 2 + 3, 5] = 80000.0
+    w[1, k - 3] = -90000.0
+    packed = oracle.quantize(w)
+    x = rows(1, xt, m, k)
+    nout = n // 2 if gated else n
+    r = rows(2, "f32", m, nout)
+    y = dev(r, gpu).clone()
+    q4lib.q4_linear(dev(x, gpu), dev(torch.from_numpy(packed), gpu), activation="relu", gated=gated, residual=y, y=y)
+    v, err = product64(x, torch.from_numpy(decode(packed, n, k)), None, "relu", gated, rounded=m > 32, scaled=xt == "bf16")
+    v, err = finish64(v, err, r, torch.float32)
+    check(y, v, err, f"m{m} n{n} k{k} {xt}")
+
+
+@pytest.mark.parametrize("m", [4, 200])
+@pytest.mark.parametrize("scale", [1e-30, 1e-6, 1e6, 1e25])
+def test_linear_bf16_rows_of_any_magnitude(q4lib, gpu, m, scale):
+    """bf16 rows far beyond fp16's range, rows of zeros, and rows that mix
+    magnitudes: every row to its own precision."""
+    n, k = 130, 512
+    packed, w = weights(3, n, k)
+    x = rows(4, "f32", m, k, scale=scale)
+    x[1] = 0
+    x[2] = 0
+    x[2, 7] = scale
+    x[3, ::2] *= 1e-4
+    x[3, 5] = 1e-13 * scale  # below 2^-32 of the row's largest
+    x = x.to(torch.bfloat16)
+    y = q4lib.q4_linear(dev(x, gpu), dev(packed, gpu), y_dtype=torch.float32)
+    v, err = product64(x, w, None, "none", False, rounded=m > 32, scaled=True)
+    v, err = finish64(v, err, None, torch.float32)
+    check(y, v, err + 1e-42, f"m{m} scale {scale}")
