@@ -47,6 +47,7 @@ COMMON_FLAGS = [
 PER_FILE_FLAGS = {
     "q4_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "q4_gemv_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "q4_fused_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -170,8 +170,9 @@ bool many_rows(int64_t m, int64_t topk, int64_t experts) {
 size_t product_workspace_bytes(int64_t m, int64_t topk, int64_t experts, int64_t n, int64_t k,
                                int64_t x_rows, DType xt, bool gated, bool combine) {
   size_t b = 0;
-  if (many_rows(m, topk, experts)) {
-    if (xt == DType::BF16) b += stage_bytes(x_rows, k);
+  const bool many = many_rows(m, topk, experts);
+  if (xt == DType::BF16 && (many || fused_gemv_supports(n, k, x_rows, experts))) b += stage_bytes(x_rows, k);
+  if (many) {
     b += fused_gemm_bytes(m, n, k, xt, gated, experts != 0);
   }
   if (combine) b += up256(static_cast<size_t>(m * topk) * static_cast<size_t>(gated ? n / 2 : n) * 4);
@@ -189,7 +190,8 @@ hipError_t launch_product(const Product& p, void* workspace, hipStream_t s) {
     ws += up256(static_cast<size_t>(p.m * p.topk) * static_cast<size_t>(ep.ldy) * 4);
   }
   hipError_t e = hipSuccess;
-  if (many_rows(p.m, p.topk, p.experts)) {
+  const bool many = many_rows(p.m, p.topk, p.experts);
+  if (many || (p.xt != DType::F32 && fused_gemv_supports(p.n, p.k, p.x_rows, p.experts))) {
     const half_t* xs = static_cast<const half_t*>(p.x);
     const float* scale = nullptr;
     if (p.xt == DType::BF16) {
@@ -197,8 +199,10 @@ hipError_t launch_product(const Product& p, void* workspace, hipStream_t s) {
       if (e != hipSuccess) return e;
       ws += stage_bytes(p.x_rows, p.k);
     }
-    const int64_t tiles = p.experts == 0 ? 0 : plan_layout(p.m, p.topk, p.experts).max_tiles;
-    e = launch_fused_gemm(p, ep, plan_rows(p), xs, scale, tiles, ws, s);
+    PlanLayout L{};
+    if (p.experts != 0) L = plan_layout(p.m, p.topk, p.experts);
+    if (many) e = launch_fused_gemm(p, ep, plan_rows(p), xs, scale, L.max_tiles, ws, s);
+    else e = launch_fused_gemv(p, ep, plan_rows(p), xs, scale, L.max_tiles, L.tile_rows, s);
   } else if (p.xt == DType::F32) {
     e = launch_row<float>(p, ep, s);
   } else if (p.xt == DType::F16) {

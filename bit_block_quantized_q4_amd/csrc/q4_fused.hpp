@@ -148,6 +148,11 @@ size_t fused_gemm_bytes(int64_t m, int64_t n, int64_t k, DType xt, bool gated, b
 hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
                              const float* xscale, int64_t row_tiles, void* workspace, hipStream_t s);
 
+// Matrix-core products of few rows (16-bit x as fp16).
+bool fused_gemv_supports(int64_t n, int64_t k, int64_t x_rows, int64_t experts);
+hipError_t launch_fused_gemv(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
+                             const float* xscale, int64_t max_tiles, int tile_rows, hipStream_t s);
+
 struct RouteArgs {
   const void* logits;
   DType dt;

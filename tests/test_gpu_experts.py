@@ -172,3 +172,11 @@ def run_moe(q4lib, gpu, m, topk, E, hidden, inter, xt, seed=0, score="softmax", 
     (64, 4, 8, 512, 352, "bf16"), (200, 2, 4, 256, 512, "f16"), (3, 2, 4, 96, 32, "f32"), (40, 1, 3, 544, 96, "bf16")])
 def test_moe_is_its_operators_in_a_row(q4lib, gpu, m, topk, E, hidden, inter, xt):
     run_moe(q4lib, gpu, m, topk, E, hidden, inter, xt)
+
+
+@pytest.mark.parametrize("m,topk,E,n,k", [(2, 2, 3, 3000, 256), (16, 2, 12, 1000, 448), (60, 1, 6, 520, 320),
+                                          (30, 2, 4, 900, 1088), (5, 8, 32, 200, 2048), (8, 3, 64, 24, 4096)])
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+def test_experts_decode_row_tiles(q4lib, gpu, m, topk, E, n, k, xt):
+    run_experts(q4lib, gpu, m, topk, E, n, k, xt, gated=True, act="silu", residual=True, seed=m)
+    run_experts(q4lib, gpu, m, topk, E, n, k, xt, combine=True, bias=True, seed=m)

@@ -115,3 +115,13 @@ def test_linear_bf16_rows_of_any_magnitude(q4lib, gpu, m, scale):
     v, err = product64(x, w, None, "none", False, rounded=m > 32, scaled=True)
     v, err = finish64(v, err, None, torch.float32)
     check(y, v, err + 1e-42, f"m{m} scale {scale}")
+
+
+@pytest.mark.parametrize("m,n,k", [(10, 33290, 512), (9, 45000, 256), (16, 28004, 320), (14, 40000, 128),
+                                   (32, 17000, 512), (20, 30000, 128), (4, 9000, 1024), (2, 5120, 2048),
+                                   (12, 20480, 192), (7, 12288, 4160), (10, 34816, 64)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_decode_row_tiles(q4lib, gpu, m, n, k, gated):
+    """Wide layers: every number of row tiles per workgroup, both ring depths,
+    two workgroups per compute unit, several rounds; short last phases."""
+    run_linear(q4lib, gpu, m, n, k, "f16" if m % 2 else "bf16", act="silu", gated=gated, residual=True, seed=m)
