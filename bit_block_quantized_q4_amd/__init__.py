@@ -187,11 +187,12 @@ def _torch():
 
 def _dtype_code(t) -> int:
     torch = _torch()
-    if t.dtype == torch.float32:
+    dtype = t.dtype
+    if dtype == torch.float32:
         return Q4_F32
-    if t.dtype == torch.float16:
+    if dtype == torch.float16:
         return Q4_F16
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return Q4_BF16
     raise TypeError(f"unsupported dtype {t.dtype}; libq4 takes float32, float16 or bfloat16")
 
@@ -318,23 +319,38 @@ def _code(table, value, what):
 
 
 def _same_device(x, **others):
+    """Refuse host and non-contiguous tensors and tensors of several devices;
+    the device's index."""
     _need_device(x, "x")
+    index = x.get_device()
     for name, t in others.items():
         if t is not None:
-            _need_device(t, name)
-            if t.device != x.device:
+            if not t.is_cuda or not t.is_contiguous():
+                _need_device(t, name)
+            if t.get_device() != index:
                 raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+    return index
+
+
+def _launch(index, stream, what, fn, *args):
+    """fn(*args, stream) with device `index` current (launches go there)."""
+    torch = _torch()
+    if stream is None:
+        handle = torch.cuda.current_stream(index).cuda_stream
+    else:
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != Q4_OK:
+        raise Q4Error(status, what)
 
 
 def _need_packed(packed, name="packed"):
     if packed.dtype != _torch().uint8:
         raise TypeError(f"{name} must be uint8; got {packed.dtype}")
-
-
-def _on(device):
-    """A context in which `device` is the current one (launches go there)."""
-    torch = _torch()
-    return torch.cuda.device(device)
 
 
 def _full_out(y, shape, dtype, device):
@@ -390,7 +406,7 @@ def q4_linear(x, packed, bias=None, activation="none", gated=False, residual=Non
     x [m, k] fp32, fp16 or bf16; packed [n, k/32*18] uint8; bias [n]; residual of
     y's shape and dtype (it may be y itself).  activation: none, relu, gelu (tanh
     form), gelu_erf or silu.  y defaults to x's dtype."""
-    _same_device(x, packed=packed, bias=bias, residual=residual, y=y, workspace=workspace)
+    index = _same_device(x, packed=packed, bias=bias, residual=residual, y=y, workspace=workspace)
     _need_packed(packed)
     n, k = packed_shape(packed)
     if x.dim() != 2 or x.shape[1] != k:
@@ -402,10 +418,8 @@ def q4_linear(x, packed, bias=None, activation="none", gated=False, residual=Non
     L = lib()
     workspace, wptr, wbytes = _workspace(
         workspace, L.q4_linear_workspace_size(m, n, k, xd, ep.gated), x.device)
-    with _on(x.device):
-        _check(L.q4_linear(x.data_ptr(), xd, packed.data_ptr(), ctypes.byref(ep), y.data_ptr(),
-                           _dtype_code(y), m, n, k, wptr, wbytes, _stream_handle(stream, x.device)),
-               "q4_linear")
+    _launch(index, stream, "q4_linear", L.q4_linear, x.data_ptr(), xd, packed.data_ptr(),
+            ctypes.byref(ep), y.data_ptr(), _dtype_code(y), m, n, k, wptr, wbytes)
     return y
 
 
@@ -473,7 +487,7 @@ def q4_route(logits, topk, score="softmax", bias=None, groups=1, group_topk=1, g
     logit of -inf or NaN is not chosen, and a place without an expert is id -1,
     weight 0."""
     torch = _torch()
-    _same_device(logits, bias=bias, ids=ids, weights=weights)
+    index = _same_device(logits, bias=bias, ids=ids, weights=weights)
     if logits.dim() != 2:
         raise ValueError(f"logits must be [m, experts]; got {tuple(logits.shape)}")
     m, experts, topk = int(logits.shape[0]), int(logits.shape[1]), int(topk)
@@ -481,24 +495,21 @@ def q4_route(logits, topk, score="softmax", bias=None, groups=1, group_topk=1, g
     plan = _new_plan(m, topk, experts, logits.device)
     ids = _ids_out(ids, (m, topk), torch.int32, logits.device, "ids")
     weights = _ids_out(weights, (m, topk), torch.float32, logits.device, "weights")
-    with _on(logits.device):
-        _check(lib().q4_route(logits.data_ptr(), _dtype_code(logits), m, experts, topk, ctypes.byref(r),
-                              ids.data_ptr(), weights.data_ptr(), plan.words.data_ptr(),
-                              _stream_handle(stream, logits.device)), "q4_route")
+    _launch(index, stream, "q4_route", lib().q4_route, logits.data_ptr(), _dtype_code(logits), m, experts,
+            topk, ctypes.byref(r), ids.data_ptr(), weights.data_ptr(), plan.words.data_ptr())
     return ids, weights, plan
 
 
 def q4_route_plan(ids, experts, stream=None):
     """The plan of given ids [m, topk] int32; ids outside 0 .. experts - 1 name no expert."""
     torch = _torch()
-    _need_device(ids, "ids")
+    index = _same_device(ids)
     if ids.dtype != torch.int32 or ids.dim() != 2:
         raise ValueError(f"ids must be int32 [m, topk]; got {ids.dtype} {tuple(ids.shape)}")
     m, topk = int(ids.shape[0]), int(ids.shape[1])
     plan = _new_plan(m, topk, int(experts), ids.device)
-    with _on(ids.device):
-        _check(lib().q4_route_plan(ids.data_ptr(), m, topk, int(experts), plan.words.data_ptr(),
-                                   _stream_handle(stream, ids.device)), "q4_route_plan")
+    _launch(index, stream, "q4_route_plan", lib().q4_route_plan, ids.data_ptr(), m, topk, int(experts),
+            plan.words.data_ptr())
     return plan
 
 
@@ -527,7 +538,7 @@ def q4_experts(x, packed, plan, bias=None, activation="none", gated=False, weigh
     were (not written); with weights [m, topk] fp32 y is [m, nout], the weighted
     sum over a token's experts.  The residual has y's shape and dtype."""
     torch = _torch()
-    _same_device(x, packed=packed, bias=bias, plan=plan.words, weights=weights, residual=residual, y=y,
+    index = _same_device(x, packed=packed, bias=bias, plan=plan.words, weights=weights, residual=residual, y=y,
                  workspace=workspace)
     experts, n, k = _expert_shape(packed)
     m, topk = plan.m, plan.topk
@@ -546,11 +557,9 @@ def q4_experts(x, packed, plan, bias=None, activation="none", gated=False, weigh
     workspace, wptr, wbytes = _workspace(
         workspace, L.q4_experts_workspace_size(m, topk, experts, n, k, x_rows, xd, ep.gated,
                                                0 if weights is None else 1), x.device)
-    with _on(x.device):
-        _check(L.q4_experts(x.data_ptr(), xd, x_rows, packed.data_ptr(), ctypes.byref(ep),
-                            plan.words.data_ptr(), None if weights is None else weights.data_ptr(),
-                            y.data_ptr(), _dtype_code(y), m, topk, experts, n, k, wptr, wbytes,
-                            _stream_handle(stream, x.device)), "q4_experts")
+    _launch(index, stream, "q4_experts", L.q4_experts, x.data_ptr(), xd, x_rows, packed.data_ptr(),
+            ctypes.byref(ep), plan.words.data_ptr(), None if weights is None else weights.data_ptr(),
+            y.data_ptr(), _dtype_code(y), m, topk, experts, n, k, wptr, wbytes)
     return y
 
 
@@ -571,7 +580,7 @@ def q4_moe(x, logits, up, down, topk, activation="silu", gated=True, up_bias=Non
     the products have x's dtype.  Routing options as in q4_route; ids and weights
     receive the routing if given."""
     torch = _torch()
-    _same_device(x, logits=logits, up=up, down=down, up_bias=up_bias, down_bias=down_bias,
+    index = _same_device(x, logits=logits, up=up, down=down, up_bias=up_bias, down_bias=down_bias,
                  residual=residual, route_bias=route_bias, ids=ids, weights=weights, y=y,
                  workspace=workspace)
     experts, nup, hidden = _expert_shape(up, "up")
@@ -598,11 +607,9 @@ def q4_moe(x, logits, up, down, topk, activation="silu", gated=True, up_bias=Non
     L = lib()
     workspace, wptr, wbytes = _workspace(
         workspace, L.q4_moe_workspace_size(m, topk, experts, hidden, inter, xd, up_ep.gated), x.device)
-    with _on(x.device):
-        _check(L.q4_moe(x.data_ptr(), xd, logits.data_ptr(), _dtype_code(logits), ctypes.byref(r),
-                        up.data_ptr(), ctypes.byref(up_ep), down.data_ptr(), ctypes.byref(down_ep),
-                        y.data_ptr(), _dtype_code(y), m, topk, experts, hidden, inter,
-                        None if ids is None else ids.data_ptr(),
-                        None if weights is None else weights.data_ptr(), wptr, wbytes,
-                        _stream_handle(stream, x.device)), "q4_moe")
+    _launch(index, stream, "q4_moe", L.q4_moe, x.data_ptr(), xd, logits.data_ptr(), _dtype_code(logits),
+            ctypes.byref(r), up.data_ptr(), ctypes.byref(up_ep), down.data_ptr(), ctypes.byref(down_ep),
+            y.data_ptr(), _dtype_code(y), m, topk, experts, hidden, inter,
+            None if ids is None else ids.data_ptr(), None if weights is None else weights.data_ptr(), wptr,
+            wbytes)
     return y

@@ -166,7 +166,7 @@ q4_status check_routing(const void* logits, int logits_dtype, int64_t m, int64_t
                         const q4_routing* r) {
   if (!logits || !r) return Q4_ERR_INVALID_ARG;
   if (!valid_pairs(m, topk, experts) || topk > experts) return Q4_ERR_SHAPE;
-  if (r->groups < 1 || experts % r->groups != 0 || r->group_topk < 1 || r->group_topk > r->groups)
+  if (r->groups < 1 || r->groups > Q4_MAX_GROUPS || experts % r->groups != 0 || r->group_topk < 1 || r->group_topk > r->groups)
     return Q4_ERR_SHAPE;
   if (!valid_in_dtype(logits_dtype)) return Q4_ERR_DTYPE;
   if ((r->score != Q4_SCORE_SOFTMAX && r->score != Q4_SCORE_SIGMOID) ||

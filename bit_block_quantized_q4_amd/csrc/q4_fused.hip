@@ -113,22 +113,55 @@ __global__ __launch_bounds__(256) void fused_row_kernel(const XT* __restrict__ x
 }
 
 // y[i] = sum_j weights[i, j] rows[i topk + j] + residual[i] in the order of j;
-// a pair whose pos is negative has no expert and counts 0.  One column per
-// thread.
+// a pair whose pos is negative has no expert and counts 0.  A workgroup takes
+// 256 V columns of one token, so weights and places are uniform, and the loads
+// of up to eight rows are in flight together.
+template <int V>
 __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part,
                                                       const float* __restrict__ weights,
-                                                      const int* __restrict__ pos, int64_t m,
-                                                      int topk, int64_t nout, Epi ep) {
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (at >= m * nout) return;
-  const int64_t i = at / nout, c = at - i * nout;
-  float v = 0.f;
-  for (int j = 0; j < topk; ++j) {
-    const int64_t p = i * topk + j;
-    if (pos[p] >= 0) v = fmaf(weights[p], part[p * nout + c], v);
+                                                      const int* __restrict__ pos, int topk,
+                                                      int64_t nout, int cblocks, Epi ep) {
+  const int64_t i = blockIdx.x / cblocks;
+  const int64_t c = (static_cast<int64_t>(blockIdx.x - i * cblocks) * 256 + threadIdx.x) * V;
+  if (c >= nout) return;
+  float v[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = 0.f;
+  const float* p0 = part + i * topk * nout + c;
+  for (int j0 = 0; j0 < topk; j0 += 8) {
+    float r[8][V];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int at = j0 + j;
+      const bool live = at < topk && pos[i * topk + (at < topk ? at : 0)] >= 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) r[j][e] = 0.f;
+      if (live) {
+        if constexpr (V == 4) {
+          const float4_t q = *reinterpret_cast<const float4_t*>(p0 + at * nout);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[j][e] = q[e];
+        } else {
+          r[j][0] = p0[at * nout];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int at = j0 + j;
+      if (at < topk && pos[i * topk + at] >= 0) {
+        const float w = weights[i * topk + at];
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = fmaf(w, r[j][e], v[e]);
+      }
+    }
   }
-  if (ep.residual != nullptr) v += load_f32(ep.residual, ep.y_dt, at);
-  store_as(ep.y, ep.y_dt, at, v);
+  const int64_t at = i * nout + c;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    if (ep.residual != nullptr) v[e] += load_f32(ep.residual, ep.y_dt, at + e);
+    store_as(ep.y, ep.y_dt, at + e, v[e]);
+  }
 }
 
 Rows plan_rows(const Product& p) {
@@ -214,12 +247,14 @@ hipError_t launch_product(const Product& p, void* workspace, hipStream_t s) {
   const PlanLayout L = plan_layout(p.m, p.topk, p.experts);
   const float* w = p.weights;
   const int* pos = p.plan + L.pos;
-  int64_t m = p.m, nout = ep.ldy;
-  int topk = static_cast<int>(p.topk);
+  int64_t nout = ep.ldy;
+  const int v = nout % 4 == 0 ? 4 : 1;
+  int topk = static_cast<int>(p.topk), cblocks = static_cast<int>((nout + 256 * v - 1) / (256 * v));
   Epi out = p.ep;
-  void* argv[] = {&part, &w, &pos, &m, &topk, &nout, &out};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&combine_kernel),
-                         dim3(static_cast<unsigned>((m * nout + 255) / 256)), dim3(256), argv, 0, s);
+  void* argv[] = {&part, &w, &pos, &topk, &nout, &cblocks, &out};
+  const void* fn = v == 4 ? reinterpret_cast<const void*>(&combine_kernel<4>)
+                          : reinterpret_cast<const void*>(&combine_kernel<1>);
+  return hipLaunchKernel(fn, dim3(static_cast<unsigned>(p.m * cblocks)), dim3(256), argv, 0, s);
 }
 
 }  // namespace q4

@@ -47,10 +47,14 @@ struct PlanLayout {
 // Rows per tile of the expert products, by the mean number of rows per
 // expert alone, so that one plan serves every product over it: 16 (one
 // activation tile of the matrix-core decode kernel) up to 12 rows, 32 up to
-// 40, then the 128-row tiles of the prefill kernel.
+// 40, then the 128-row tiles of the prefill kernel, and from 80 on the experts'
+// own tile of 192 rows (128 experts, 128 rows on average, 2048 x 2048 gated:
+// 232 us against 305 us with 128-row tiles; at a mean of 96 the two are equal).
+constexpr int kGroupRows = 192;
+
 inline int expert_tile_rows(int64_t m, int64_t topk, int64_t experts) {
   const double mean = static_cast<double>(m) * static_cast<double>(topk) / static_cast<double>(experts);
-  return mean <= 12.0 || m <= 16 ? 16 : mean <= 40.0 || m <= 32 ? 32 : 128;
+  return mean <= 12.0 || m <= 16 ? 16 : mean <= 40.0 || m <= 32 ? 32 : mean <= 80.0 ? 128 : kGroupRows;
 }
 
 inline PlanLayout plan_layout(int64_t m, int64_t topk, int64_t experts) {

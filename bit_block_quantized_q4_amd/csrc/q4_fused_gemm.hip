@@ -16,7 +16,7 @@
 // multiples of 2^-39 of it (finer than what the fp32 sums keep of the row).
 #include "q4_fused.hpp"
 #include "q4_gemm_plan.hpp"
-#include "q4_gemm_tile.hpp"
+#include "q4_gemm_group.hpp"
 
 namespace q4 {
 namespace {
@@ -60,13 +60,14 @@ struct FusedArgs {
   int64_t c0;           // first tile column of this launch
   float* part;          // PART: split-K partials, [z][m][ldp]
   int64_t ldp, zstride;
+  int parts;            // experts: kernel tiles per tile of the plan
 };
 
 enum Mode { kDense = 0, kGrouped = 1, kPart = 2 };
 
-template <int BM, bool GATED, int MODE>
+template <int BM, bool GATED, int MODE, bool DEALT = false>
 struct FusedIO {
-  static constexpr bool kPlain = false;
+  static constexpr bool kPlain = false, kDealt = DEALT;
   static constexpr bool kPairs = GATED && MODE != kPart;
   FusedArgs a;
   int* prow;      // LDS: row of y of every tile row
@@ -91,11 +92,13 @@ struct FusedIO {
     static_assert(TM == BM, "tile rows");
     n0 = a.c0 + static_cast<int64_t>(blockIdx.x) * TN;
     if constexpr (MODE == kGrouped) {
-      const int t = blockIdx.y;
+      const int t = blockIdx.y / a.parts;
       if (t >= *a.rows.ntiles) return false;
       const int4 tile = a.rows.tiles[t];
-      m0 = tile.y;
-      count = tile.z;
+      const int skip = (blockIdx.y - t * a.parts) * BM, left = tile.z - skip;
+      if (left <= 0) return false;
+      m0 = tile.y + skip;
+      count = left < BM ? left : BM;
       woff = tile.x * a.rows.wstride;
       boff = tile.x * a.rows.nbias;
     } else {
@@ -124,6 +127,9 @@ struct FusedIO {
       return (u < a.ep.half ? u : a.ep.half - 1) + ((g >> 5) & 1) * a.ep.half;
     }
     return g < a.cols ? g : a.cols - 1;
+  }
+  __device__ __forceinline__ int fragments(int rows) const {
+    return __builtin_amdgcn_readfirstlane((count + rows - 1) / rows);
   }
   __device__ __forceinline__ bool row_in(int r) const { return r < count; }
   __device__ __forceinline__ bool col_in(int c) const {
@@ -244,6 +250,18 @@ __global__ __launch_bounds__(WVM * WVN * 64, 1) void fused_mfma_kernel(const hal
   gemm_mfma_body<BM, BN, WVM, WVN>(FusedIO<BM, GATED, MODE>{a, prow, pscale, votes}, x, W, k, kps, xe, xet);
 }
 
+template <bool GATED>
+__global__ __launch_bounds__(512, 1) void fused_group_kernel(const half_t* __restrict__ x,
+                                                             const uint8_t* __restrict__ W, int64_t k, int,
+                                                             FusedArgs a, const void* __restrict__ xe,
+                                                             int xet) {
+  __shared__ int prow[kGroupRows];
+  __shared__ float pscale[kGroupRows];
+  __shared__ uint32_t votes[4];
+  gemm_group_body<kGroupRows, 256, 2, 4>(
+      FusedIO<kGroupRows, GATED, kGrouped, true>{a, prow, pscale, votes}, x, W, k, xe, xet);
+}
+
 template <bool GATED, int MODE>
 __global__ __launch_bounds__(256, 1) void fused_slicek_kernel(const half_t* __restrict__ x,
                                                               const uint8_t* __restrict__ W, int64_t k,
@@ -359,8 +377,8 @@ template <bool GATED, int MODE>
 KernelFn kernel_of(Tile t) {
   if constexpr (MODE != kGrouped) {
     if (t == Tile::Big) return reinterpret_cast<KernelFn>(&fused_mfma_kernel<256, 256, 2, 4, GATED, MODE>);
+    if (t == Tile::SliceK) return reinterpret_cast<KernelFn>(&fused_slicek_kernel<GATED, MODE>);
   }
-  if (t == Tile::SliceK) return reinterpret_cast<KernelFn>(&fused_slicek_kernel<GATED, MODE>);
   return reinterpret_cast<KernelFn>(&fused_mfma_kernel<128, 128, 2, 2, GATED, MODE>);
 }
 
@@ -407,8 +425,11 @@ size_t fused_gemm_bytes(int64_t m, int64_t n, int64_t k, DType xt, bool gated, b
 hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
                              const float* xscale, int64_t row_tiles, void* workspace, hipStream_t s) {
   const bool gated = ep.half != 0, grouped = rows.order != nullptr;
-  FusedArgs a{ep, rows, xscale, p.m, tile_cols(p.n, gated), 0, nullptr, 0, 0};
+  FusedArgs a{ep, rows, xscale, p.m, tile_cols(p.n, gated), 0, nullptr, 0, 0, 1};
   const int xet = static_cast<int>(p.xt);
+  const int plan_rows = grouped ? plan_layout(p.m, p.topk, p.experts).tile_rows : 128;
+  a.parts = (plan_rows + 127) / 128;  // of the kernels of 128-row tiles
+  if (grouped) row_tiles *= a.parts;
   const int mode = grouped ? kGrouped : kDense;
   if (p.xt == DType::F32) {
     const KernelFn fn =
@@ -430,12 +451,15 @@ hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, 
   }
   const int nks = static_cast<int>(p.k / kBK);
   if (grouped) {
-    // Slice-K tiles address x and the expert's weights with 32-bit offsets.
-    const bool sk = p.k % 256 == 0 && p.k >= 1024 && p.x_rows * p.k * 2 < (int64_t{1} << 32) &&
-                    p.n * (p.k / kQK) * kBlockBytes < (int64_t{1} << 32);
-    const Tile t = sk ? Tile::SliceK : Tile::Out128;
-    return launch_tiles(gated ? kernel_in<true>(t, mode) : kernel_in<false>(t, mode), 128, 256, xs, p.W, p.k,
-                        nks, a, a.cols, row_tiles, 1, p.x, xet, s);
+    if (plan_rows == kGroupRows) {
+      row_tiles /= a.parts;
+      a.parts = 1;
+      return launch_tiles(gated ? reinterpret_cast<KernelFn>(&fused_group_kernel<true>)
+                                : reinterpret_cast<KernelFn>(&fused_group_kernel<false>),
+                          256, 512, xs, p.W, p.k, nks, a, a.cols, row_tiles, 1, p.x, xet, s);
+    }
+    return launch_tiles(gated ? kernel_in<true>(Tile::Out128, mode) : kernel_in<false>(Tile::Out128, mode), 128,
+                        256, xs, p.W, p.k, nks, a, a.cols, row_tiles, 1, p.x, xet, s);
   }
   const GemmPlan g = gemm_plan(p.m, a.cols, p.k);
   auto threads = [](Tile t) { return t == Tile::Big ? 512 : 256; };

@@ -16,6 +16,8 @@
 //   columns<W>(c0)     what this thread needs of its 8 columns of W from c0
 //   emit<SCALED>(cols, sums, r)  the outputs of tile row r in those columns
 //   votes              LDS words, one per chunk of rows, zero at the end of K
+// kDealt: fragment i of wave row w holds tile rows 32 (i WVM + w) .. instead of
+//   32 (w TM + i) ..; fragments(n) says how many fragments of n rows hold rows.
 // kPairs: tile columns c and c + 32 (c / 32 even) make one output.
 #pragma once
 
@@ -68,9 +70,10 @@ __device__ __forceinline__ void each_chunk(F&& f) {
 // is not finite; tile_row(i, r) is the tile row of its row r.  A chunk with
 // such a sum is not stored (the residual may be the output, which the exact
 // route must find unchanged): its bit is set in the result, uniform over the
-// workgroup.
+// workgroup.  live: chunks that hold rows.
 template <int CHUNKS, int NTH, int BN, int RCH, bool SCALED, typename IO, typename W, typename R>
-__device__ __forceinline__ uint32_t fused_epilogue(const IO& io, float* buf, int c0, W write, R tile_row) {
+__device__ __forceinline__ uint32_t fused_epilogue(const IO& io, float* buf, int c0, W write, R tile_row,
+                                                   int live = CHUNKS) {
   constexpr int kGroups = IO::kPairs ? BN / 16 : BN / 8;  // threads per row
   constexpr int kStep = NTH / kGroups;
   const int g = threadIdx.x % kGroups;
@@ -79,6 +82,7 @@ __device__ __forceinline__ uint32_t fused_epilogue(const IO& io, float* buf, int
   uint32_t skipped = 0;
   each_chunk<0, CHUNKS>([&](auto ic) {
     constexpr int i = decltype(ic)::value;
+    if (i >= live) return;  // no rows
     __syncthreads();  // the buffer's previous readers are done
     if (write(ic)) io.votes[i] = 1u;  // every writer writes the same value
     __syncthreads();
@@ -103,8 +107,8 @@ __device__ __forceinline__ uint32_t fused_epilogue(const IO& io, float* buf, int
 template <int NTH, typename IO>
 __device__ __forceinline__ void exact_tile128(const IO& io, const void* x, DType xt, int64_t ldx,
                                               const uint8_t* W, int64_t rb, int r0, int c0, int64_t b0,
-                                              int64_t b1, float* lds, int period = 128,
-                                              uint32_t chunks = ~0u) {
+                                              int64_t b1, float* lds, int chunk_rows = 128,
+                                              int chunk_mask = 0, uint32_t chunks = ~0u) {
   static_assert(NTH == 256 || NTH == 512, "four or eight waves");
   constexpr int WVM = NTH == 512 ? 4 : 2;  // waves along the rows
   constexpr int TI = 4 / WVM;              // 32-row products per wave
@@ -167,7 +171,7 @@ __device__ __forceinline__ void exact_tile128(const IO& io, const void* x, DType
           io.store1(r0 + wm * 32 * TI + 32 * i + 8 * (r / 4) + 4 * (lane >> 5) + (r & 3),
                     c0 + wn * 64 + 32 * j + (lane & 31), acc[i][j][r]);
   } else {
-    // Stores the rows whose chunk (row % period / 32) is asked for.
+    // Stores the rows whose chunk (row / chunk_rows & chunk_mask) is asked for.
     const auto cols = io.template columns<128>(c0, threadIdx.x % (IO::kPairs ? 8 : 16));
     constexpr int kGroups = IO::kPairs ? 8 : 16;
     const int g = threadIdx.x % kGroups, at = IO::kPairs ? 64 * (g >> 2) + 8 * (g & 3) : 8 * g;
@@ -184,22 +188,24 @@ __device__ __forceinline__ void exact_tile128(const IO& io, const void* x, DType
 #pragma unroll 1
       for (int r = tid / kGroups; r < 32 * WVM; r += NTH / kGroups) {
         const int row = r0 + (r >> 5) * 32 * TI + 32 * q + (r & 31);
-        if ((chunks >> ((row & (period - 1)) >> 5)) & 1) io.template emit<false>(cols, lds + r * 132 + at, row);
+        if ((chunks >> ((row / chunk_rows) & chunk_mask)) & 1) io.template emit<false>(cols, lds + r * 132 + at, row);
       }
     });
   }
 }
 
-// A BMT x BNT tile (multiples of 128) on the exact route, 128 x 128 at a time.
+// A BMT x BNT tile (BNT a multiple of 128) on the exact route, 128 x 128 at a time.
 template <int NTH, int BMT, int BNT, typename IO>
 __device__ __forceinline__ void exact_tile(const IO& io, const void* x, DType xt, int64_t ldx,
                                            const uint8_t* W, int64_t rb, int64_t b0, int64_t b1,
-                                           float* lds, int period, uint32_t chunks) {
+                                           float* lds, int chunk_rows, int chunk_mask,
+                                           uint32_t chunks) {
 #pragma unroll 1
-  for (int ti = 0; ti < BMT / 128; ++ti)
+  for (int ti = 0; ti < (BMT + 127) / 128; ++ti)
 #pragma unroll 1
     for (int tj = 0; tj < BNT / 128; ++tj)
-      exact_tile128<NTH>(io, x, xt, ldx, W, rb, 128 * ti, 128 * tj, b0, b1, lds, period, chunks);
+      exact_tile128<NTH>(io, x, xt, ldx, W, rb, 128 * ti, 128 * tj, b0, b1, lds, chunk_rows,
+                         chunk_mask, chunks);
 }
 
 // Stores the workgroup's WVM x WVN waves' TM x TN products of 32 x 32.  32 x 32
@@ -209,7 +215,7 @@ __device__ __forceinline__ void exact_tile(const IO& io, const void* x, DType xt
 // what it stored, a fused one has left out the chunks asked for.
 template <int WVM, int WVN, int TM, int TN, typename IO, typename F>
 __device__ __forceinline__ void store_tile(const IO& io, const float16_t (&acc)[TM][TN], uint8_t* lds,
-                                           F exact) {
+                                           F exact, int live = TM) {
   const int wave = threadIdx.x >> 6;
   const int wm = wave / WVN, wn = wave % WVN;
   const int r0 = wm * 32 * TM, c0 = wn * 32 * TN;
@@ -244,7 +250,10 @@ __device__ __forceinline__ void store_tile(const IO& io, const float16_t (&acc)[
             }
           return odd;
         },
-        [&](int i, int r) { return (r >> 5) * 32 * TM + 32 * i + (r & 31); });
+        [&](int i, int r) {
+          return IO::kDealt ? 32 * WVM * i + r : (r >> 5) * 32 * TM + 32 * i + (r & 31);
+        },
+        live);
     if (skipped != 0) exact(skipped);
   }
 }
@@ -342,7 +351,7 @@ __device__ __forceinline__ void gemm_tile_body(IO io, const half_t* __restrict__
 
   store_tile<2, 2>(io, acc, tsm, [&](uint32_t chunks) {
     exact_tile128<256>(io, xe, static_cast<DType>(xet), k, W, nb * kBlockBytes, 0, 0, 0, nb,
-                       reinterpret_cast<float*>(tsm), 64, chunks);
+                       reinterpret_cast<float*>(tsm), 32, 1, chunks);
   });
 }
 
@@ -623,7 +632,8 @@ __device__ __forceinline__ void gemm_mfma_body(IO io, const half_t* __restrict__
   // store, measured slower: each store then touches 32 rows.)
   store_tile<WVM, WVN>(io, acc, smem, [&](uint32_t chunks) {
     exact_tile<NTH, BM, BN>(io, xe, static_cast<DType>(xet), k, W0, rb, 2 * static_cast<int64_t>(ks0),
-                            2 * static_cast<int64_t>(ks0 + nks), reinterpret_cast<float*>(smem), WM, chunks);
+                            2 * static_cast<int64_t>(ks0 + nks), reinterpret_cast<float*>(smem), 32, TM - 1,
+                            chunks);
   });
 }
 
@@ -909,7 +919,7 @@ __device__ __forceinline__ void gemm_slicek_body(IO io, const half_t* __restrict
   const int rb4 = tid & 7, cb4 = tid >> 3;
   auto exact = [&](uint32_t chunks) {
     exact_tile128<256>(io, xe, static_cast<DType>(xet), k, W0, rb, 0, 0, 2 * static_cast<int64_t>(ks0),
-                       2 * static_cast<int64_t>(ks0 + nks), reinterpret_cast<float*>(smem), 128, chunks);
+                       2 * static_cast<int64_t>(ks0 + nks), reinterpret_cast<float*>(smem), 32, 3, chunks);
   };
   // One 32-row chunk: the waves' partials column-major, then their sums
   // (columns 4 cb4 .. + 3, rows 4 rb4 .. + 3 of the chunk).

@@ -242,6 +242,7 @@ q4_status q4_linear(const void *x, int x_dtype, const void *packed,
 
 #define Q4_MAX_EXPERTS 1024
 #define Q4_MAX_TOPK 32
+#define Q4_MAX_GROUPS 64
 
 typedef enum q4_score { Q4_SCORE_SOFTMAX = 0, Q4_SCORE_SIGMOID = 1 } q4_score;
 typedef enum q4_group_score {
@@ -266,7 +267,7 @@ typedef enum q4_group_score {
 typedef struct q4_routing {
   int score;         /* q4_score */
   const float *bias; /* [experts] fp32 device array, 4-byte aligned; NULL: none */
-  int groups;        /* >= 1, divides experts */
+  int groups;        /* 1 .. Q4_MAX_GROUPS, divides experts */
   int group_topk;    /* 1 .. groups */
   int group_score;   /* q4_group_score; read when groups > 1 */
   int renormalise;   /* 0 or 1 */
