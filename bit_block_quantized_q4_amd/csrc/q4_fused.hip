@@ -53,11 +53,13 @@ __global__ __launch_bounds__(256) void fused_row_kernel(const XT* __restrict__ x
   const int64_t t = blockIdx.x / cblocks;
   const int64_t c = (blockIdx.x - t * cblocks) * 4 + threadIdx.x / kWave;
   if (c >= nout) return;  // whole wavefront
-  int64_t start = 0, count = m, boff = 0;
-  if (rows.order != nullptr) {
+  int64_t count = m, boff = 0;
+  const int* rec = nullptr;
+  if (rows.recs != nullptr) {
     if (t >= *rows.ntiles) return;
-    const int4 tile = rows.tiles[t];
-    start = tile.y;
+    rec = rows.recs + t * rows.rec_words;
+    const int4 tile = *reinterpret_cast<const int4*>(rec);
+    rec += 4;
     count = tile.z;
     W += tile.x * rows.wstride;
     boff = tile.x * rows.nbias;
@@ -72,10 +74,15 @@ __global__ __launch_bounds__(256) void fused_row_kernel(const XT* __restrict__ x
     int64_t yrow[kRowMT];
 #pragma unroll
     for (int i = 0; i < kRowMT; ++i) {
-      const int64_t at = start + r0 + (i < mt ? i : mt - 1);  // rows past the last repeat it
-      const int64_t p = rows.order != nullptr ? rows.order[at] : at;
-      yrow[i] = p;
-      xr[i] = x + (rows.order != nullptr ? p / rows.xdiv : p) * k;
+      const int64_t at = r0 + (i < mt ? i : mt - 1);  // rows past the last repeat it
+      yrow[i] = at;
+      int64_t from = at;
+      if (rec != nullptr) {
+        const int p = rec[at];
+        yrow[i] = p;
+        from = p / rows.xdiv;
+      }
+      xr[i] = x + from * k;
     }
     float acc[G][kRowMT];
 #pragma unroll
@@ -168,9 +175,9 @@ Rows plan_rows(const Product& p) {
   Rows r;
   if (p.experts == 0) return r;
   const PlanLayout L = plan_layout(p.m, p.topk, p.experts);
-  r.order = p.plan + L.order;
+  r.recs = p.plan + L.tiles;
   r.ntiles = p.plan + L.head;
-  r.tiles = reinterpret_cast<const int4*>(p.plan + L.tiles);
+  r.rec_words = L.rec_words;
   r.xdiv = p.x_rows == p.m ? static_cast<int>(p.topk) : 1;
   r.wstride = p.n * (p.k / kQK) * kBlockBytes;
   r.nbias = p.n;

@@ -19,14 +19,14 @@ struct Epi {
   int bias_dt = 0, act = 0, y_dt = 0;
 };
 
-// Which rows of x a product takes.  order == nullptr: one group, rows 0 ..
-// m - 1 of x and y.  Otherwise tile t of the plan covers the pairs
-// order[start .. start + count - 1] of one expert; pair p reads row p / xdiv
-// of x and writes row p of y.
+// Which rows of x a product takes.  recs == nullptr: one group, rows 0 .. m - 1
+// of x and y.  Otherwise tile t is the plan's record t: {expert, first place,
+// rows, 0} and then its pairs; pair p reads row p / xdiv of x and writes row p
+// of y.
 struct Rows {
-  const int* order = nullptr;
+  const int* recs = nullptr;
   const int* ntiles = nullptr;  // tiles in use (the grid is an upper bound)
-  const int4* tiles = nullptr;  // {expert, start, count, 0}
+  int rec_words = 0;
   int xdiv = 1;
   int64_t wstride = 0;  // packed bytes per expert
   int64_t nbias = 0;    // bias values per expert
@@ -36,12 +36,13 @@ struct Rows {
 //
 // Device layout of a plan in int32 words: offsets[experts + 1], order[pairs],
 // pos[pairs] (the place of a pair in `order`, -1 without an expert), {ntiles,
-// rows per tile, 0, 0}, tiles of four words.  Every part starts at a multiple
-// of four words.
+// rows per tile, 0, 0}, and the tiles' records: {expert, first place, rows, 0}
+// and `tile_rows` pairs (a product's workgroup finds all it needs to start in
+// one place).  Every part starts at a multiple of four words.
 struct PlanLayout {
   int64_t order, pos, head, tiles, words;
   int64_t max_tiles;
-  int tile_rows;
+  int tile_rows, rec_words;
 };
 
 // Rows per tile of the expert products, by the mean number of rows per
@@ -68,7 +69,8 @@ inline PlanLayout plan_layout(int64_t m, int64_t topk, int64_t experts) {
   p.pos = p.order + up4(pairs);
   p.head = p.pos + up4(pairs);
   p.tiles = p.head + 4;
-  p.words = p.tiles + 4 * p.max_tiles;
+  p.rec_words = 4 + p.tile_rows;
+  p.words = p.tiles + p.rec_words * p.max_tiles;
   return p;
 }
 

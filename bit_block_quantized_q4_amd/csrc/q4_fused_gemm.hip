@@ -74,6 +74,7 @@ struct FusedIO {
   float* pscale;  // LDS: factor of its sums
   uint32_t* votes;  // LDS: chunks of rows with a sum that is not finite
   int64_t n0 = 0, m0 = 0, boff = 0, woff = 0;
+  const int* rec = nullptr;  // kGrouped: the tile's pairs
   int count = 0;
 
   // A thread's eight output columns.
@@ -93,11 +94,12 @@ struct FusedIO {
     n0 = a.c0 + static_cast<int64_t>(blockIdx.x) * TN;
     if constexpr (MODE == kGrouped) {
       const int t = blockIdx.y / a.parts;
-      if (t >= *a.rows.ntiles) return false;
-      const int4 tile = a.rows.tiles[t];
+      rec = a.rows.recs + static_cast<int64_t>(t) * a.rows.rec_words;
+      const int4 tile = *reinterpret_cast<const int4*>(rec);
+      const int used = *a.rows.ntiles;  // (both loads in flight)
       const int skip = (blockIdx.y - t * a.parts) * BM, left = tile.z - skip;
-      if (left <= 0) return false;
-      m0 = tile.y + skip;
+      if (t >= used || left <= 0) return false;
+      rec += 4 + skip;
       count = left < BM ? left : BM;
       woff = tile.x * a.rows.wstride;
       boff = tile.x * a.rows.nbias;
@@ -109,16 +111,15 @@ struct FusedIO {
     if (threadIdx.x < 4) votes[threadIdx.x] = 0u;
     for (int r = threadIdx.x; r < BM; r += blockDim.x) {
       const int64_t x = xrow(r);
-      if constexpr (MODE == kGrouped) prow[r] = a.rows.order[m0 + (r < count ? r : count - 1)];
+      if constexpr (MODE == kGrouped) prow[r] = rec[r < count ? r : 0];
       pscale[r] = a.xscale != nullptr ? a.xscale[x] : 1.0f;
     }
     return true;  // (read after the tile loop's barriers)
   }
   __device__ __forceinline__ const uint8_t* weights(const uint8_t* W) const { return W + woff; }
   __device__ __forceinline__ int64_t xrow(int r) const {
-    const int64_t at = m0 + (r < count ? r : count - 1);
-    if constexpr (MODE == kGrouped) return a.rows.order[at] / a.rows.xdiv;
-    return at;
+    if constexpr (MODE == kGrouped) return rec[r < count ? r : 0] / a.rows.xdiv;
+    return m0 + (r < count ? r : count - 1);
   }
   __device__ __forceinline__ int64_t wrow(int c) const {
     const int64_t g = n0 + c;
@@ -424,7 +425,7 @@ size_t fused_gemm_bytes(int64_t m, int64_t n, int64_t k, DType xt, bool gated, b
 
 hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
                              const float* xscale, int64_t row_tiles, void* workspace, hipStream_t s) {
-  const bool gated = ep.half != 0, grouped = rows.order != nullptr;
+  const bool gated = ep.half != 0, grouped = rows.recs != nullptr;
   FusedArgs a{ep, rows, xscale, p.m, tile_cols(p.n, gated), 0, nullptr, 0, 0, 1};
   const int xet = static_cast<int>(p.xt);
   const int plan_rows = grouped ? plan_layout(p.m, p.topk, p.experts).tile_rows : 128;

@@ -45,15 +45,26 @@ __global__ __launch_bounds__((NW + NP) * kWave, 1) void fused_gemv_kernel(const 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int tile = blockIdx.x / a.cblocks;
   const int64_t col0 = static_cast<int64_t>(blockIdx.x - tile * a.cblocks) * a.cols;
-  int64_t start = 0, boff = 0;
+  int64_t boff = 0;
   int m = a.m;
-  if (a.rows.order != nullptr) {
+  // Rows of y and factors of the tile's rows, behind the ring (thread r keeps
+  // row r's until the end).
+  int* const yrows = reinterpret_cast<int*>(tsm + G::lds);
+  float* const factors = reinterpret_cast<float*>(yrows + 16 * AT);
+  const int* const rec = a.rows.recs != nullptr ? a.rows.recs + static_cast<int64_t>(tile) * a.rows.rec_words : nullptr;
+  int pair = threadIdx.x;
+  if (rec != nullptr) {
+    const int4 t = *reinterpret_cast<const int4*>(rec);
+    if (threadIdx.x < 16 * AT) pair = rec[4 + threadIdx.x];  // (all three loads in flight)
     if (tile >= *a.rows.ntiles) return;
-    const int4 t = a.rows.tiles[tile];
-    start = t.y;
     m = t.z;
     W += t.x * a.rows.wstride;
     boff = t.x * a.rows.nbias;
+  }
+  if (static_cast<int>(threadIdx.x) < m) {
+    yrows[threadIdx.x] = pair;
+    const int64_t row = rec != nullptr ? pair / a.rows.xdiv : pair;
+    factors[threadIdx.x] = a.xscale != nullptr ? a.xscale[row] : 1.0f;
   }
   const int nc = static_cast<int>(a.nout - col0 < a.cols ? a.nout - col0 : a.cols);  // columns stored
   const int rv = GATED ? 2 * nc : nc;                                               // weight rows copied
@@ -109,8 +120,8 @@ __global__ __launch_bounds__((NW + NP) * kWave, 1) void fused_gemv_kernel(const 
       const int i = (q * CW + cwave) * kWave + lane;
       const int ar = i / G::xp;
       const int pc = (i - ar * G::xp) ^ (ar & 15);
-      const int64_t at = start + (ar < m ? ar : 0);
-      const int64_t row = a.rows.order != nullptr ? a.rows.order[at] / a.rows.xdiv : at;
+      const int at = ar < m ? ar : 0;
+      const int64_t row = rec != nullptr ? rec[4 + at] / a.rows.xdiv : at;
       xsrc[q] = static_cast<uint32_t>((row * k + 8 * pc) * 2);
       const bool f = ar < m, l = f && pc < 4 * last;
       xfull |= f ? 1u << q : 0u;
@@ -251,13 +262,8 @@ __global__ __launch_bounds__((NW + NP) * kWave, 1) void fused_gemv_kernel(const 
   const float* rf = reinterpret_cast<const float*>(tsm);
   for (int o = threadIdx.x; o < nc * m; o += G::lanes) {
     const int ar = o / nc, c = o - ar * nc;
-    const int64_t at = start + ar;
-    int64_t row = at, xr = at;
-    if (a.rows.order != nullptr) {
-      row = a.rows.order[at];
-      xr = row / a.rows.xdiv;
-    }
-    const float sc = a.xscale != nullptr ? a.xscale[xr] : 1.0f;
+    const int64_t row = yrows[ar];
+    const float sc = factors[ar];
     auto sum = [&](int r) {
       const float* q = rf + ((((r >> 4) * AT + (ar >> 4)) * NW) * kWave + (r & 15) + 16 * ((ar >> 2) & 3)) * 4 + (ar & 3);
       float s = 0.f;
@@ -282,11 +288,12 @@ struct Form {
 template <int T, int AT, int PB, int NW = 8, int NP = 4, int WR = 16 * T, int XR = 16 * AT>
 Form form() {
   using G = TileGeo<T, AT, PB, NW, NP, WR, XR>;
-  static_assert(G::lds <= kTLdsMax, "LDS budget");
+  constexpr int kLds = G::lds + 16 * AT * 8;  // the ring, and the rows' table
+  static_assert(kLds <= kTLdsMax, "LDS budget");
   static std::atomic<uint64_t> allowed[2];
   return Form{{reinterpret_cast<KernelFn>(&fused_gemv_kernel<T, AT, PB, NW, NP, WR, XR, false>),
                reinterpret_cast<KernelFn>(&fused_gemv_kernel<T, AT, PB, NW, NP, WR, XR, true>)},
-              WR, G::lds, G::lanes, allowed};
+              WR, kLds, G::lanes, allowed};
 }
 
 // Two workgroups per compute unit: 8-block phases, four computing and two
@@ -294,7 +301,7 @@ Form form() {
 template <int T, int AT>
 Form pair_form() {
   using G = TileGeo<T, AT, 8, 4, 2>;
-  static_assert(2 * G::lds <= kTLdsMax, "two workgroups per compute unit");
+  static_assert(2 * (G::lds + 16 * AT * 8) <= kTLdsMax, "two workgroups per compute unit");
   return form<T, AT, 8, 4, 2>();
 }
 
@@ -409,7 +416,7 @@ bool fused_gemv_supports(int64_t n, int64_t k, int64_t x_rows, int64_t experts) 
 
 hipError_t launch_fused_gemv(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
                              const float* xscale, int64_t max_tiles, int tile_rows, hipStream_t s) {
-  const bool gated = ep.half != 0, grouped = rows.order != nullptr;
+  const bool gated = ep.half != 0, grouped = rows.recs != nullptr;
   const int64_t pairs = p.m * p.topk;
   const int at = (grouped ? tile_rows : p.m) > 16 ? 2 : 1;
   const int64_t tiles = grouped ? (pairs < p.experts ? pairs : p.experts) : 1;

@@ -289,11 +289,21 @@ __device__ __forceinline__ void scan_experts(PlanLds& s, int experts, int tile_r
 // Tiles of expert e (c pairs from place `first`), written by one wavefront.
 __device__ __forceinline__ void write_tiles(int e, int first, int c, int tile0, const PlanLayout& L,
                                             int* plan) {
-  int4* tiles = reinterpret_cast<int4*>(plan + L.tiles);
   for (int i = threadIdx.x & (kWave - 1); i * L.tile_rows < c; i += kWave) {
     const int left = c - i * L.tile_rows;
-    tiles[tile0 + i] = int4{e, first + i * L.tile_rows, left < L.tile_rows ? left : L.tile_rows, 0};
+    *reinterpret_cast<int4*>(plan + L.tiles + static_cast<int64_t>(tile0 + i) * L.rec_words) =
+        int4{e, first + i * L.tile_rows, left < L.tile_rows ? left : L.tile_rows, 0};
   }
+}
+
+// Pair p is the r-th of its expert, whose places start at `first` and whose
+// tiles at tile0.
+__device__ __forceinline__ void place_pair(int p, int r, int first, int tile0, const PlanLayout& L,
+                                           int* plan) {
+  plan[L.order + first + r] = p;
+  plan[L.pos + p] = first + r;
+  const int t = r / L.tile_rows;
+  plan[L.tiles + static_cast<int64_t>(tile0 + t) * L.rec_words + 4 + (r - t * L.tile_rows)] = p;
 }
 
 // The whole plan of at most kThreads pairs whose counts are in s.total, by one
@@ -333,9 +343,12 @@ __device__ __forceinline__ void plan_one(PlanLds& s, const int* ids, int pairs, 
       rank += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
     }
     rank += __popcll(same & ((uint64_t{1} << (tid & (kWave - 1))) - 1));
-    const int at = s.base[id] + rank;
-    plan[L.order + at] = id < experts ? tid : -1;
-    plan[L.pos + tid] = id < experts ? at : -1;
+    if (id < experts) {
+      place_pair(tid, rank, s.base[id], s.tile0[id], L, plan);
+    } else {
+      plan[L.order + s.base[id] + rank] = -1;
+      plan[L.pos + tid] = -1;
+    }
   }
 }
 
@@ -448,7 +461,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(const int* __restrict__ 
     }
   }
   __syncthreads();
-  const int first = first_s;
+  const int first = first_s, tile0 = tile_s;
   int count = 0, before = 0;  // before: in the earlier wavefronts' shares
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
@@ -460,12 +473,12 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(const int* __restrict__ 
   if (tid == 0) {
     plan[me] = first;
     if (rest) {
-      plan[L.head] = tile_s;
+      plan[L.head] = tile0;
       plan[L.head + 1] = L.tile_rows;
     }
   }
-  if (!rest && wave == 0) write_tiles(me, first, count, tile_s, L, plan);
-  int at = first + before;
+  if (!rest && wave == 0) write_tiles(me, first, count, tile0, L, plan);
+  int at = before;
   for (int c0 = 0; c0 < chunks; c0 += kAhead) {
     int id[kAhead];
     load(c0, id);
@@ -474,9 +487,13 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(const int* __restrict__ 
       const uint64_t mask = __ballot(id[u] == me);
       if (id[u] == me) {
         const int p = p0 + (c0 + u) * kWave + lane;
-        const int to = at + __popcll(mask & ((uint64_t{1} << lane) - 1));
-        plan[L.order + to] = rest ? -1 : p;
-        plan[L.pos + p] = rest ? -1 : to;
+        const int r = at + __popcll(mask & ((uint64_t{1} << lane) - 1));
+        if (rest) {
+          plan[L.order + first + r] = -1;
+          plan[L.pos + p] = -1;
+        } else {
+          place_pair(p, r, first, tile0, L, plan);
+        }
       }
       at += __popcll(mask);
     }
