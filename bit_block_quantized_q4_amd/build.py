@@ -48,6 +48,7 @@ PER_FILE_FLAGS = {
     "q4_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "q4_gemv_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "q4_fused_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "q4_fused_wave.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -94,6 +94,29 @@ __device__ __forceinline__ void store_as(void* p, int dt, int64_t i, float v) {
   else static_cast<uint16_t*>(p)[i] = f32_to_16(v, dt);
 }
 
+// Staging a bf16 row as fp16: the largest magnitude (as bf16 bits) so far, the
+// power of two that brings it to [2^15, 2^16) (at most 2^126; none for rows of
+// zeros or with an infinity or NaN), and two values times that power, rounded
+// to nearest even.
+__device__ __forceinline__ uint32_t max_magnitude_bf16(uint32_t top, uint32_t v) {
+  const uint32_t lo = v & 0x7FFFu, hi = (v >> 16) & 0x7FFFu;
+  const uint32_t b = lo > hi ? lo : hi;
+  return b > top ? b : top;
+}
+__device__ __forceinline__ int bf16_row_shift(uint32_t top) {
+  const int e = static_cast<int>(top >> 7);  // top = 1.f 2^(e - 127)
+  const int shift = e == 0xFF || top == 0 ? 0 : 142 - e;
+  return shift > 126 ? 126 : shift;
+}
+__device__ __forceinline__ float power_of_two(int s) {
+  return __builtin_bit_cast(float, static_cast<uint32_t>(127 + s) << 23);
+}
+__device__ __forceinline__ uint32_t bf16x2_scaled_to_f16x2(uint32_t v, float f) {
+  const half2_t h = {static_cast<half_t>(bf16_bits_to_float(v & 0xFFFFu) * f),
+                     static_cast<half_t>(__builtin_bit_cast(float, v & 0xFFFF0000u) * f)};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
 // silu and the tanh form of gelu as z / (1 + exp(-t)): no cancellation for
 // negative z, and 0 (not NaN) where exp overflows.
 __device__ __forceinline__ float activate(float z, int act) {
@@ -158,6 +181,12 @@ hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, 
 bool fused_gemv_supports(int64_t n, int64_t k, int64_t x_rows, int64_t experts);
 hipError_t launch_fused_gemv(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
                              const float* xscale, int64_t max_tiles, int tile_rows, hipStream_t s);
+
+// Expert products of at most 16 rows per tile, streamed by single wavefronts.
+// They take bf16 x as it is.
+bool fused_wave_supports(int64_t m, int64_t topk, int64_t experts, int64_t n, int64_t k, int64_t x_rows);
+hipError_t launch_fused_wave(const Product& p, const Epi& ep, const Rows& rows, int64_t max_tiles,
+                             hipStream_t s);
 
 struct RouteArgs {
   const void* logits;

@@ -334,11 +334,7 @@ __global__ __launch_bounds__(256) void stage_bf16_kernel(const uint16_t* __restr
   for (int64_t p = threadIdx.x; p < np; p += 256) {
     const u32x4 v = src[p];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = v[e] & 0x7FFFu, hi = (v[e] >> 16) & 0x7FFFu;
-      const uint32_t b = lo > hi ? lo : hi;
-      top = b > top ? b : top;
-    }
+    for (int e = 0; e < 4; ++e) top = max_magnitude_bf16(top, v[e]);
   }
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
@@ -349,20 +345,13 @@ __global__ __launch_bounds__(256) void stage_bf16_kernel(const uint16_t* __restr
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 4; ++w) top = top_s[w] > top ? top_s[w] : top;
-  // top = 1.f 2^(E - 127): factor 2^(15 - (E - 127)), at most 2^126.
-  const int E = static_cast<int>(top >> 7);
-  int sh = E == 0xFF || top == 0 ? 0 : 142 - E;
-  if (sh > 126) sh = 126;
-  const float f = __builtin_bit_cast(float, static_cast<uint32_t>(127 + sh) << 23);
-  if (threadIdx.x == 0) inv[row] = __builtin_bit_cast(float, static_cast<uint32_t>(127 - sh) << 23);
+  const int shift = bf16_row_shift(top);
+  const float f = power_of_two(shift);
+  if (threadIdx.x == 0) inv[row] = power_of_two(-shift);
   for (int64_t p = threadIdx.x; p < np; p += 256) {
     u32x4 v = src[p];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const half2_t h = {static_cast<half_t>(bf16_bits_to_float(v[e] & 0xFFFFu) * f),
-                         static_cast<half_t>(__builtin_bit_cast(float, v[e] & 0xFFFF0000u) * f)};
-      v[e] = __builtin_bit_cast(uint32_t, h);
-    }
+    for (int e = 0; e < 4; ++e) v[e] = bf16x2_scaled_to_f16x2(v[e], f);
     dst[p] = v;
   }
 }

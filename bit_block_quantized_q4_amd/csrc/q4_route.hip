@@ -15,7 +15,7 @@
 // Plan: a stable counting sort of the pairs by expert.  One workgroup per
 // expert counts the earlier experts' pairs in an LDS histogram (integer adds:
 // their order does not matter) and places its own in ascending order by
-// ballots.  Up to 64 tokens run as one workgroup and one launch.
+// ballots.  Up to 16 tokens run as one workgroup and one launch.
 //
 // Bound by latency and by the instructions of the choice: 4096 tokens of 256
 // experts are 2 MB of logits (0.4 us at 5 TB/s) and 0.6 MB of outputs.
@@ -27,7 +27,7 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxExperts = 1024;
-constexpr int kOneTokens = 64;  // most tokens of a single-workgroup routing,
+constexpr int kOneTokens = 16;  // most tokens of a single-workgroup routing,
 constexpr int kOnePerLane = 4;  // and most experts per lane (its waves' LDS)
 
 struct RouteParams {

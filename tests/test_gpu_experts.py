@@ -180,3 +180,14 @@ def test_moe_is_its_operators_in_a_row(q4lib, gpu, m, topk, E, hidden, inter, xt
 def test_experts_decode_row_tiles(q4lib, gpu, m, topk, E, n, k, xt):
     run_experts(q4lib, gpu, m, topk, E, n, k, xt, gated=True, act="silu", residual=True, seed=m)
     run_experts(q4lib, gpu, m, topk, E, n, k, xt, combine=True, bias=True, seed=m)
+
+
+@pytest.mark.parametrize("m,topk,E,n,k", [(9, 4, 64, 130, 512), (2, 8, 16, 72, 448), (24, 2, 16, 264, 1024)])
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+def test_experts_named_often_by_a_token(q4lib, gpu, m, topk, E, n, k, xt):
+    """Tokens that name one expert in all their places: more rows in its tiles
+    than there are tokens."""
+    ids = torch.full((m, topk), 3, dtype=torch.int32)
+    ids[m // 2] = torch.arange(topk, dtype=torch.int32)
+    run_experts(q4lib, gpu, m, topk, E, n, k, xt, gated=True, act="silu", ids=ids, seed=m)
+    run_experts(q4lib, gpu, m, topk, E, n, k, xt, combine=True, residual=True, ids=ids, seed=m)
