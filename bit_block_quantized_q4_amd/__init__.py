@@ -311,6 +311,29 @@ def q4_gemm_noalloc(x, packed, y, stream=None, n=None, k=None):
 
 # ------------------------------------------------------------ fused layers
 
+_FAST = None  # the native short way (_q4_torch), or False where it is not built
+
+
+def _fast():
+    """The native module that takes ordinary calls (no y, workspace or stream of
+    the caller's) the short way; None where it is not built.  It returns None
+    for a call that it does not take, which then goes the full way here."""
+    global _FAST
+    if _FAST is None:
+        L = lib()
+        try:
+            from . import _q4_torch
+        except ImportError:
+            _FAST = False
+        else:
+            _q4_torch.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+                "q4_linear", "q4_linear_workspace_size", "q4_route", "q4_route_plan",
+                "q4_route_plan_size", "q4_experts", "q4_experts_workspace_size", "q4_moe",
+                "q4_moe_workspace_size")))
+            _FAST = _q4_torch
+    return _FAST or None
+
+
 def _code(table, value, what):
     try:
         return table[value]
@@ -406,6 +429,12 @@ def q4_linear(x, packed, bias=None, activation="none", gated=False, residual=Non
     x [m, k] fp32, fp16 or bf16; packed [n, k/32*18] uint8; bias [n]; residual of
     y's shape and dtype (it may be y itself).  activation: none, relu, gelu (tanh
     form), gelu_erf or silu.  y defaults to x's dtype."""
+    if y is None and y_dtype is None and workspace is None and stream is None:
+        fast = _FAST or _fast()
+        if fast is not None:
+            out = fast.linear(x, packed, bias, ACTIVATIONS.get(activation), gated, residual)
+            if out is not None:
+                return out
     index = _same_device(x, packed=packed, bias=bias, residual=residual, y=y, workspace=workspace)
     _need_packed(packed)
     n, k = packed_shape(packed)
@@ -486,6 +515,13 @@ def q4_route(logits, topk, score="softmax", bias=None, groups=1, group_topk=1, g
     weights [m, topk] fp32, plan); ties go to the lowest index, an expert with a
     logit of -inf or NaN is not chosen, and a place without an expert is id -1,
     weight 0."""
+    if ids is None and weights is None and stream is None:
+        fast = _FAST or _fast()
+        if fast is not None:
+            out = fast.route(logits, topk, bias, SCORES.get(score), groups, group_topk,
+                             GROUP_SCORES.get(group_score), renormalise, scale)
+            if out is not None:
+                return out[0], out[1], Plan(out[2], logits.shape[0], topk, logits.shape[1])
     torch = _torch()
     index = _same_device(logits, bias=bias, ids=ids, weights=weights)
     if logits.dim() != 2:
@@ -502,6 +538,12 @@ def q4_route(logits, topk, score="softmax", bias=None, groups=1, group_topk=1, g
 
 def q4_route_plan(ids, experts, stream=None):
     """The plan of given ids [m, topk] int32; ids outside 0 .. experts - 1 name no expert."""
+    if stream is None:
+        fast = _FAST or _fast()
+        if fast is not None:
+            words = fast.route_plan(ids, experts)
+            if words is not None:
+                return Plan(words, ids.shape[0], ids.shape[1], experts)
     torch = _torch()
     index = _same_device(ids)
     if ids.dtype != torch.int32 or ids.dim() != 2:
@@ -537,6 +579,13 @@ def q4_experts(x, packed, plan, bias=None, activation="none", gated=False, weigh
     is [m * topk, nout], and rows of pairs without an expert are left as they
     were (not written); with weights [m, topk] fp32 y is [m, nout], the weighted
     sum over a token's experts.  The residual has y's shape and dtype."""
+    if y is None and y_dtype is None and workspace is None and stream is None:
+        fast = _FAST or _fast()
+        if fast is not None:
+            out = fast.experts(x, packed, plan.words, plan.m, plan.topk, plan.experts, bias,
+                               ACTIVATIONS.get(activation), gated, weights, residual)
+            if out is not None:
+                return out
     torch = _torch()
     index = _same_device(x, packed=packed, bias=bias, plan=plan.words, weights=weights, residual=residual, y=y,
                  workspace=workspace)
@@ -579,6 +628,15 @@ def q4_moe(x, logits, up, down, topk, activation="silu", gated=True, up_bias=Non
     and add the rows up by the routing weights, plus the residual.  The rows between
     the products have x's dtype.  Routing options as in q4_route; ids and weights
     receive the routing if given."""
+    if (y is None and y_dtype is None and workspace is None and stream is None and ids is None
+            and weights is None):
+        fast = _FAST or _fast()
+        if fast is not None:
+            out = fast.moe(x, logits, up, down, topk, ACTIVATIONS.get(activation), gated, up_bias,
+                           down_bias, residual, route_bias, SCORES.get(score), groups, group_topk,
+                           GROUP_SCORES.get(group_score), renormalise, scale)
+            if out is not None:
+                return out
     torch = _torch()
     index = _same_device(x, logits=logits, up=up, down=down, up_bias=up_bias, down_bias=down_bias,
                  residual=residual, route_bias=route_bias, ids=ids, weights=weights, y=y,

@@ -25,6 +25,8 @@ HOST_LIB_PATH = PKG / "libq4host.so"
 FLOOR_SRCS = (PKG / "floor" / "q4_read_floor.hip", PKG / "floor" / "q4_mfma_ceiling.hip")
 FLOOR_LIB_PATH = PKG / "libq4floor.so"
 TRACE_LIB_PATH = PKG / "libq4trace.so"
+TORCH_SRC = PKG / "binding" / "q4_torch.cpp"
+TORCH_LIB_PATH = PKG / "_q4_torch.so"
 ARCH = os.environ.get("Q4_OFFLOAD_ARCH", "gfx950")
 
 COMMON_FLAGS = [
@@ -87,6 +89,27 @@ def build_host(verbose: bool = False) -> Path:
     return HOST_LIB_PATH
 
 
+def build_torch(verbose: bool = False) -> Path:
+    """Compile the fused calls' short way from Python (binding/q4_torch.cpp, host
+    code against torch's headers) into _q4_torch.so; returns its path."""
+    import sysconfig
+
+    import torch
+    base = Path(torch.__file__).parent
+    cxx = os.environ.get("CXX", "g++")
+    tmp = TORCH_LIB_PATH.with_suffix(".so.tmp")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D__HIP_PLATFORM_AMD__=1",
+          "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+          f"-I{sysconfig.get_paths()['include']}", f"-I{base / 'include'}",
+          f"-I{base / 'include' / 'torch' / 'csrc' / 'api' / 'include'}",
+          f"-I{os.environ.get('ROCM_PATH', '/opt/rocm')}/include", f"-I{INCLUDE}", str(TORCH_SRC),
+          "-o", str(tmp), f"-L{base / 'lib'}", "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_hip"],
+         verbose)
+    os.replace(tmp, TORCH_LIB_PATH)
+    return TORCH_LIB_PATH
+
+
 def build_floor(verbose: bool = False) -> Path:
     """Compile the benchmark's measurement kernels (floor/: the plain read and
     the matrix-core ceiling) into libq4floor.so; returns its path."""
@@ -116,9 +139,10 @@ def build_trace(verbose: bool = False) -> Path:
 
 def build(verbose: bool = False) -> Path:
     """Compile every csrc/*.hip for gfx950 and link libq4.so (and build the
-    host-CPU twin libq4host.so and the benchmark's measurement libq4floor.so);
-    returns libq4.so's path."""
+    host-CPU twin libq4host.so, the torch binding's _q4_torch.so and the benchmark's
+    measurement libq4floor.so); returns libq4.so's path."""
     build_host(verbose)
+    build_torch(verbose)
     build_floor(verbose)
     hipcc = _hipcc()
     BUILD_DIR.mkdir(exist_ok=True)

@@ -181,3 +181,25 @@ def test_options_of_the_binding_match_the_header():
         named = {k.lower(): int(v) for k, v in re.findall(prefix + r"([A-Z0-9_]+) = (\d+)", text)}
         assert named == table
     assert f"#define Q4_MAX_EXPERTS {q4.MAX_EXPERTS}" in text and f"#define Q4_MAX_TOPK {q4.MAX_TOPK}" in text
+
+
+def test_native_binding_leaves_what_it_does_not_take_to_python(q4lib):
+    """The short way answers None (and the Python function raises) for host
+    tensors, wrong shapes and options; nothing is launched."""
+    torch = pytest.importorskip("torch")
+    fast = q4lib._fast()
+    assert fast is not None, "the native binding is built with the library"
+    x, packed = torch.zeros(4, 64, dtype=torch.float16), torch.zeros(8, 36, dtype=torch.uint8)
+    assert fast.linear(x, packed, None, 0, False, None) is None
+    assert fast.linear(x, packed, None, None, False, None) is None
+    assert fast.linear(None, packed, None, 0, False, None) is None
+    assert fast.linear(x, 3, None, 0, False, None) is None
+    assert fast.linear(x) is None
+    assert fast.route(torch.zeros(2, 8), 2, None, 0, 1, 1, 0, True, 1.0) is None
+    assert fast.route_plan(torch.zeros(2, 2, dtype=torch.int32), 8) is None
+    assert fast.experts(x, packed, x, 4, 1, 2, None, 0, False, None, None) is None
+    assert fast.moe(*([None] * 17)) is None
+    with pytest.raises(TypeError):
+        fast.bind()
+    with pytest.raises(ValueError, match="device tensor"):
+        q4lib.q4_linear(x, packed)

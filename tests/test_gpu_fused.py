@@ -125,3 +125,33 @@ def test_linear_decode_row_tiles(q4lib, gpu, m, n, k, gated):
     """Wide layers: every number of row tiles per workgroup, both ring depths,
     two workgroups per compute unit, several rounds; short last phases."""
     run_linear(q4lib, gpu, m, n, k, "f16" if m % 2 else "bf16", act="silu", gated=gated, residual=True, seed=m)
+
+
+def test_both_ways_from_python_agree_and_refuse_alike(q4lib, gpu):
+    """A call with an output of the caller's takes the full way, one without the
+    native way: the same bits.  Calls that neither may take raise."""
+    packed, _ = weights(1, 96, 256)
+    x, b, r = rows(2, "f16", 5, 256), rows(3, "f16", 96), rows(4, "f16", 5, 48)
+    pd, xd, bd, rd = dev(packed, gpu), dev(x, gpu), dev(b, gpu), dev(r, gpu)
+    kw = dict(bias=bd, activation="silu", gated=True, residual=rd)
+    want = q4lib.q4_linear(xd, pd, y=torch.empty_like(rd), **kw)
+    assert torch.equal(q4lib.q4_linear(xd, pd, **kw), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        on_side = q4lib.q4_linear(xd, pd, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(on_side, want)
+    for bad, err in ((dict(bias=bd[:-1]), ValueError), (dict(activation="tanh"), ValueError),
+                     (dict(residual=rd.float()), ValueError), (dict(residual=rd.t()), ValueError),
+                     (dict(bias=b), ValueError)):
+        with pytest.raises(err):
+            q4lib.q4_linear(xd, pd, **{**kw, **bad})
+    with pytest.raises(ValueError):
+        q4lib.q4_linear(xd[:, ::2], pd, **kw)
+    with pytest.raises(TypeError):
+        q4lib.q4_linear(xd, pd.view(torch.int8), **kw)
+    with pytest.raises(q4lib.Q4Error):
+        q4lib.q4_route(dev(rows(5, "f32", 3, 8), gpu), 9)
+    with pytest.raises(q4lib.Q4Error):
+        q4lib.q4_route(dev(rows(5, "f32", 3, 9), gpu), 2, groups=2)
