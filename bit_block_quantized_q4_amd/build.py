@@ -51,6 +51,7 @@ PER_FILE_FLAGS = {
     "q4_gemv_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "q4_fused_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "q4_fused_wave.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "q4_moe_one.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -484,9 +484,7 @@ q4_status q4_moe(const void* x, int x_dtype, const void* logits, int logits_dtyp
   if (s2 != Q4_OK) return s2;
   if (overlaps_any(ys, {xs, us})) return Q4_ERR_INVALID_ARG;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const hipError_t e = q4::launch_route(
-      make_route(logits, logits_dtype, m, experts, topk, *routing, wids, ww, base), st);
-  if (e != hipSuccess) return Q4_ERR_HIP;
+  const q4::RouteArgs ra = make_route(logits, logits_dtype, m, experts, topk, *routing, wids, ww, base);
   q4::Product p;
   p.x = x;
   p.xt = static_cast<q4::DType>(x_dtype);
@@ -498,16 +496,19 @@ q4_status q4_moe(const void* x, int x_dtype, const void* logits, int logits_dtyp
   p.experts = experts;
   p.plan = reinterpret_cast<const int*>(base);
   p.ep = make_epi(up_epilogue, h, x_dtype, nup);
-  const hipError_t e1 = q4::launch_product(p, pw, st);
-  if (e1 != hipSuccess) return Q4_ERR_HIP;
-  p.x = h;
-  p.x_rows = m * topk;
-  p.W = static_cast<const uint8_t*>(down);
-  p.n = hidden;
-  p.k = inter;
-  p.weights = ww;
-  p.ep = make_epi(down_epilogue, y, y_dtype, hidden);
-  return from_hip(q4::launch_product(p, pw, st));
+  q4::Product d = p;
+  d.x = h;
+  d.x_rows = m * topk;
+  d.W = static_cast<const uint8_t*>(down);
+  d.n = hidden;
+  d.k = inter;
+  d.weights = ww;
+  d.ep = make_epi(down_epilogue, y, y_dtype, hidden);
+  if (q4::moe_one_supports(ra, p, d)) return from_hip(q4::launch_moe_one(ra, p, d, st));
+  hipError_t e = q4::launch_route(ra, st);
+  if (e == hipSuccess) e = q4::launch_product(p, pw, st);
+  if (e == hipSuccess) e = q4::launch_product(d, pw, st);
+  return from_hip(e);
 }
 
 }  // extern "C"

@@ -200,6 +200,10 @@ struct RouteArgs {
   int* plan;  // may be null
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+
+// An expert layer of one token (r.plan unused; up.ep.y is down.x).
+bool moe_one_supports(const RouteArgs& r, const Product& up, const Product& down);
+hipError_t launch_moe_one(const RouteArgs& r, const Product& up, const Product& down, hipStream_t s);
 hipError_t launch_route_plan(const int* ids, int64_t m, int64_t topk, int64_t experts, int* plan,
                              hipStream_t s);
 
