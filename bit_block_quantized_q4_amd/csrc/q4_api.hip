@@ -80,6 +80,9 @@ q4_status check_matmul(const void* x, int x_dtype, const void* packed, void* y,
 
 // ------------------------------------------------------------------ fused
 
+// A grid that no launch holds (launch_blocks) is a matter of the shape.
+q4_status from_launch(hipError_t e) { return e == hipErrorInvalidConfiguration ? Q4_ERR_SHAPE : from_hip(e); }
+
 constexpr int64_t kMaxPairs = int64_t(1) << 24;  // tokens x experts each
 
 struct Span {
@@ -166,7 +169,8 @@ q4_status check_routing(const void* logits, int logits_dtype, int64_t m, int64_t
                         const q4_routing* r) {
   if (!logits || !r) return Q4_ERR_INVALID_ARG;
   if (!valid_pairs(m, topk, experts) || topk > experts) return Q4_ERR_SHAPE;
-  if (r->groups < 1 || r->groups > Q4_MAX_GROUPS || experts % r->groups != 0 || r->group_topk < 1 || r->group_topk > r->groups)
+  if (r->groups < 1 || r->groups > Q4_MAX_GROUPS || experts % r->groups != 0 || r->group_topk < 1 ||
+      r->group_topk > r->groups)
     return Q4_ERR_SHAPE;
   if (!valid_in_dtype(logits_dtype)) return Q4_ERR_DTYPE;
   if ((r->score != Q4_SCORE_SOFTMAX && r->score != Q4_SCORE_SIGMOID) ||
@@ -312,7 +316,7 @@ q4_status q4_linear(const void* x, int x_dtype, const void* packed, const q4_epi
   p.n = n;
   p.k = k;
   p.ep = make_epi(epilogue, y, y_dtype, n);
-  return from_hip(q4::launch_product(p, workspace, reinterpret_cast<hipStream_t>(stream)));
+  return from_launch(q4::launch_product(p, workspace, reinterpret_cast<hipStream_t>(stream)));
 }
 
 size_t q4_route_plan_size(int64_t m, int64_t topk, int64_t experts) {
@@ -385,7 +389,7 @@ q4_status q4_experts(const void* x, int x_dtype, int64_t x_rows, const void* pac
   p.plan = static_cast<const int*>(plan);
   p.weights = weights;
   p.ep = make_epi(epilogue, y, y_dtype, n);
-  return from_hip(q4::launch_product(p, workspace, reinterpret_cast<hipStream_t>(stream)));
+  return from_launch(q4::launch_product(p, workspace, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
@@ -504,11 +508,11 @@ q4_status q4_moe(const void* x, int x_dtype, const void* logits, int logits_dtyp
   d.k = inter;
   d.weights = ww;
   d.ep = make_epi(down_epilogue, y, y_dtype, hidden);
-  if (q4::moe_one_supports(ra, p, d)) return from_hip(q4::launch_moe_one(ra, p, d, st));
+  if (q4::moe_one_supports(ra, p, d)) return from_launch(q4::launch_moe_one(ra, p, d, st));
   hipError_t e = q4::launch_route(ra, st);
   if (e == hipSuccess) e = q4::launch_product(p, pw, st);
   if (e == hipSuccess) e = q4::launch_product(d, pw, st);
-  return from_hip(e);
+  return from_launch(e);
 }
 
 }  // extern "C"

@@ -195,7 +195,7 @@ hipError_t launch_row(const Product& p, const Epi& ep0, hipStream_t s) {
   void* argv[] = {&x, &W, &m, &nout, &k, &cblocks, &ep, &rows};
   const void* fn = ep.half != 0 ? reinterpret_cast<const void*>(&fused_row_kernel<XT, 2>)
                                 : reinterpret_cast<const void*>(&fused_row_kernel<XT, 1>);
-  return hipLaunchKernel(fn, dim3(static_cast<unsigned>(cblocks * tiles)), dim3(256), argv, 0, s);
+  return launch_blocks(fn, cblocks * tiles, 256, argv, 0, s);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -211,10 +211,10 @@ size_t product_workspace_bytes(int64_t m, int64_t topk, int64_t experts, int64_t
                                int64_t x_rows, DType xt, bool gated, bool combine) {
   size_t b = 0;
   const bool many = many_rows(m, topk, experts);
-  if (xt == DType::BF16 && !fused_wave_supports(m, topk, experts, n, k, x_rows) && (many || fused_gemv_supports(n, k, x_rows, experts))) b += stage_bytes(x_rows, k);
-  if (many) {
-    b += fused_gemm_bytes(m, n, k, xt, gated, experts != 0);
-  }
+  if (xt == DType::BF16 && !fused_wave_supports(m, topk, experts, n, k, x_rows) &&
+      (many || fused_gemv_supports(n, k, x_rows, experts)))
+    b += stage_bytes(x_rows, k);
+  if (many) b += fused_gemm_bytes(m, n, k, xt, gated, experts != 0);
   if (combine) b += up256(static_cast<size_t>(m * topk) * static_cast<size_t>(gated ? n / 2 : n) * 4);
   return b;
 }
@@ -263,7 +263,7 @@ hipError_t launch_product(const Product& p, void* workspace, hipStream_t s) {
   void* argv[] = {&part, &w, &pos, &topk, &nout, &cblocks, &out};
   const void* fn = v == 4 ? reinterpret_cast<const void*>(&combine_kernel<4>)
                           : reinterpret_cast<const void*>(&combine_kernel<1>);
-  return hipLaunchKernel(fn, dim3(static_cast<unsigned>(p.m * cblocks)), dim3(256), argv, 0, s);
+  return launch_blocks(fn, p.m * cblocks, 256, argv, 0, s);
 }
 
 }  // namespace q4

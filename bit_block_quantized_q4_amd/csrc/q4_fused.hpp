@@ -96,8 +96,9 @@ __device__ __forceinline__ void store_as(void* p, int dt, int64_t i, float v) {
 
 // Staging a bf16 row as fp16: the largest magnitude (as bf16 bits) so far, the
 // power of two that brings it to [2^15, 2^16) (at most 2^126; none for rows of
-// zeros or with an infinity or NaN), and two values times that power, rounded
-// to nearest even.
+// zeros), and two values times that power, rounded to nearest even.  A row with
+// an infinity or NaN takes 2^-112, which brings every finite value into fp16:
+// its outputs are infinite or NaN by that element alone.
 __device__ __forceinline__ uint32_t max_magnitude_bf16(uint32_t top, uint32_t v) {
   const uint32_t lo = v & 0x7FFFu, hi = (v >> 16) & 0x7FFFu;
   const uint32_t b = lo > hi ? lo : hi;
@@ -105,7 +106,7 @@ __device__ __forceinline__ uint32_t max_magnitude_bf16(uint32_t top, uint32_t v)
 }
 __device__ __forceinline__ int bf16_row_shift(uint32_t top) {
   const int e = static_cast<int>(top >> 7);  // top = 1.f 2^(e - 127)
-  const int shift = e == 0xFF || top == 0 ? 0 : 142 - e;
+  const int shift = e == 0xFF ? -112 : top == 0 ? 0 : 142 - e;
   return shift > 126 ? 126 : shift;
 }
 __device__ __forceinline__ float power_of_two(int s) {
@@ -150,6 +151,16 @@ __device__ __forceinline__ void finish_store(const Epi& ep, int64_t boff, int64_
 }
 
 // ------------------------------------------------------------------ launchers
+
+// A launch of x * y * z workgroups.  One that a grid does not hold (2^32 threads
+// along x, 65535 workgroups along y or z) is refused here instead of cut short.
+inline hipError_t launch_blocks(const void* fn, int64_t x, int threads, void** argv, size_t lds, hipStream_t s,
+                                int64_t y = 1, int64_t z = 1) {
+  if (x < 1 || x > ((int64_t{1} << 32) - 1) / threads || y < 1 || y > 65535 || z < 1 || z > 65535)
+    return hipErrorInvalidConfiguration;
+  return hipLaunchKernel(fn, dim3(static_cast<unsigned>(x), static_cast<unsigned>(y), static_cast<unsigned>(z)),
+                         dim3(static_cast<unsigned>(threads)), argv, lds, s);
+}
 
 // A product as the launchers take it.
 struct Product {
@@ -200,11 +211,11 @@ struct RouteArgs {
   int* plan;  // may be null
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+hipError_t launch_route_plan(const int* ids, int64_t m, int64_t topk, int64_t experts, int* plan,
+                             hipStream_t s);
 
 // An expert layer of one token (r.plan unused; up.ep.y is down.x).
 bool moe_one_supports(const RouteArgs& r, const Product& up, const Product& down);
 hipError_t launch_moe_one(const RouteArgs& r, const Product& up, const Product& down, hipStream_t s);
-hipError_t launch_route_plan(const int* ids, int64_t m, int64_t topk, int64_t experts, int* plan,
-                             hipStream_t s);
 
 }  // namespace q4

@@ -320,8 +320,8 @@ __global__ __launch_bounds__(256) void fused_reduce_kernel(FusedArgs a, int spli
 }
 
 // bf16 rows -> fp16 rows and the inverse of their power-of-two factors; one
-// workgroup per row.  A row with an infinity or a NaN keeps factor 1 (its
-// tiles then take the exact route).
+// workgroup per row.  The sums of a row with an infinity or a NaN are not
+// finite, so its tiles take the exact route.
 __global__ __launch_bounds__(256) void stage_bf16_kernel(const uint16_t* __restrict__ x,
                                                          uint16_t* __restrict__ out,
                                                          float* __restrict__ inv, int64_t k) {
@@ -361,6 +361,11 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // Tile columns of a product.
 int64_t tile_cols(int64_t n, bool gated) { return gated ? (n / 2 + 31) / 32 * 64 : n; }
 
+// The slice-K tile reaches a gate's up rows by 32-bit offsets from the gate's.
+bool slice_k(int64_t n, int64_t k, bool gated) {
+  return !gated || n * (k / kQK * kBlockBytes) < (int64_t{1} << 32);
+}
+
 using KernelFn = const void*;
 
 template <bool GATED, int MODE>
@@ -383,9 +388,7 @@ hipError_t launch_tiles(KernelFn fn, int tile, int threads, const half_t* x, con
                         const void* xe, int xet, hipStream_t s) {
   FusedArgs a = a0;
   void* argv[] = {&x, &W, &k, &kps, &a, &xe, &xet};
-  return hipLaunchKernel(fn, dim3(static_cast<unsigned>((cols + tile - 1) / tile),
-                                  static_cast<unsigned>(row_tiles), static_cast<unsigned>(splits)),
-                         dim3(static_cast<unsigned>(threads)), argv, 0, s);
+  return launch_blocks(fn, (cols + tile - 1) / tile, threads, argv, 0, s, row_tiles, splits);
 }
 
 }  // namespace
@@ -403,13 +406,12 @@ hipError_t launch_stage(const void* x, int64_t rows, int64_t k, void* ws, const 
   *xs = reinterpret_cast<const half_t*>(dst);
   *scale = inv;
   void* argv[] = {&src, &dst, &inv, &k};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&stage_bf16_kernel),
-                         dim3(static_cast<unsigned>(rows)), dim3(256), argv, 0, s);
+  return launch_blocks(reinterpret_cast<const void*>(&stage_bf16_kernel), rows, 256, argv, 0, s);
 }
 
 size_t fused_gemm_bytes(int64_t m, int64_t n, int64_t k, DType xt, bool gated, bool grouped) {
   if (grouped || xt == DType::F32) return 0;
-  return up256(gemm_plan(m, tile_cols(n, gated), k).ws_bytes);
+  return up256(gemm_plan(m, tile_cols(n, gated), k, slice_k(n, k, gated)).ws_bytes);
 }
 
 hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
@@ -451,7 +453,7 @@ hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, 
     return launch_tiles(gated ? kernel_in<true>(Tile::Out128, mode) : kernel_in<false>(Tile::Out128, mode), 128,
                         256, xs, p.W, p.k, nks, a, a.cols, row_tiles, 1, p.x, xet, s);
   }
-  const GemmPlan g = gemm_plan(p.m, a.cols, p.k);
+  const GemmPlan g = gemm_plan(p.m, a.cols, p.k, slice_k(p.n, p.k, gated));
   auto threads = [](Tile t) { return t == Tile::Big ? 512 : 256; };
   hipError_t e = hipSuccess;
   if (g.n_main > 0) {
@@ -475,7 +477,7 @@ hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, 
   void* argv[] = {&a, &splits, &quads};
   const KernelFn fn = gated ? reinterpret_cast<KernelFn>(&fused_reduce_kernel<true>)
                             : reinterpret_cast<KernelFn>(&fused_reduce_kernel<false>);
-  return hipLaunchKernel(fn, dim3(static_cast<unsigned>((p.m * quads + 255) / 256)), dim3(256), argv, 0, s);
+  return launch_blocks(fn, (p.m * quads + 255) / 256, 256, argv, 0, s);
 }
 
 }  // namespace q4

@@ -433,8 +433,7 @@ hipError_t launch_fused_gemv(const Product& p, const Epi& ep, const Rows& rows, 
   int64_t k = p.k;
   void* argv[] = {&xs, &W, &k, &a};
   const int64_t grid = static_cast<int64_t>(a.cblocks) * (grouped ? max_tiles : 1);
-  return hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(f.form.threads)),
-                         argv, static_cast<size_t>(f.form.lds), s);
+  return launch_blocks(fn, grid, f.form.threads, argv, static_cast<size_t>(f.form.lds), s);
 }
 
 }  // namespace q4

@@ -140,8 +140,7 @@ hipError_t launch_form(const half_t* x, bool xb, const uint8_t* W, int64_t k, Wa
   const hipError_t e = allow_dynamic_lds(fns[f], kLdsMax, allowed[f]);
   if (e != hipSuccess) return e;
   void* argv[] = {&x, &W, &k, &a};
-  return hipLaunchKernel(fns[f], dim3(static_cast<unsigned>(grid)), dim3(NW * kWave), argv,
-                         static_cast<size_t>(lds), s);
+  return launch_blocks(fns[f], grid, NW * kWave, argv, static_cast<size_t>(lds), s);
 }
 
 }  // namespace

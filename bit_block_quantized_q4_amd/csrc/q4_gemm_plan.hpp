@@ -68,11 +68,13 @@ inline int split_kps(Tile t, int nks, int s) {
   return kps;
 }
 
-inline GemmPlan gemm_plan(int64_t m, int64_t n, int64_t k) {
+// slice_k: whether the slice-K tile (32-bit offsets from its first weight row)
+// may run.
+inline GemmPlan gemm_plan(int64_t m, int64_t n, int64_t k, bool slice_k = true) {
   GemmPlan best;
   const int64_t cu = device_cu_count();
   const int nks = static_cast<int>(k / kPlanBK);
-  const bool sk_ok = k % 256 == 0 && k >= 1024;  // short k: prologue and reduction dominate
+  const bool sk_ok = slice_k && k % 256 == 0 && k >= 1024;  // short k: prologue and reduction dominate
   const bool split_ok = k % kPlanBK == 0 && n % 4 == 0;
   best.main = m >= 1024 ? Tile::Big : sk_ok ? Tile::SliceK : Tile::Out128;
   best.n_main = n;

@@ -165,8 +165,7 @@ hipError_t launch(KernelFn fn, std::atomic<uint64_t>& allowed, int64_t grid, int
                   hipStream_t s) {
   const hipError_t e = allow_dynamic_lds(fn, kLdsMax, allowed);
   if (e != hipSuccess) return e;
-  return hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads)), argv,
-                         static_cast<size_t>(lds), s);
+  return launch_blocks(fn, grid, threads, argv, static_cast<size_t>(lds), s);
 }
 
 template <typename K>

@@ -203,3 +203,16 @@ def test_native_binding_leaves_what_it_does_not_take_to_python(q4lib):
         fast.bind()
     with pytest.raises(ValueError, match="device tensor"):
         q4lib.q4_linear(x, packed)
+
+
+def test_more_workgroups_than_a_launch_holds(q4lib):
+    """Refused by the launch rule itself, not cut to 32 bits."""
+    L = q4lib.lib()
+    far = ctypes.c_void_p
+    rows_, base = 65536 * 128, 1 << 40
+    x, w, y = far(base), far(base * 2), far(base * 3)
+    assert L.q4_linear(x, F32, w, ep(q4lib), y, F32, rows_, 1, 32, None, 0, None) == SHAPE
+    assert q4lib.q4_experts_workspace_size(1024, 32, 1024, 1 << 23, 32, 1024, F32) == 0
+    plan = far(base * 4)
+    assert L.q4_experts(x, F32, 1024, w, ep(q4lib), plan, None, y, F32, 1024, 32, 1024, 1 << 23, 32, None, 0,
+                        None) == SHAPE
