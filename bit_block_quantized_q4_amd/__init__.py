@@ -355,13 +355,24 @@ def _same_device(x, **others):
     return index
 
 
-def _launch(index, stream, what, fn, *args):
-    """fn(*args, stream) with device `index` current (launches go there)."""
+def _on(stream, x):
+    """A context in which `stream` (a torch stream or a handle) is the current one
+    of x's device: what a call allocates then belongs to that stream, and is used
+    again only by work behind the call's."""
     torch = _torch()
-    if stream is None:
-        handle = torch.cuda.current_stream(index).cuda_stream
-    else:
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
+    _need_device(x, "x")
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=x.device) if stream
+                  else torch.cuda.default_stream(x.device))
+    if stream.device != x.device:
+        raise ValueError(f"stream is on {stream.device}, x on {x.device}")
+    return torch.cuda.stream(stream)
+
+
+def _launch(index, what, fn, *args):
+    """fn(*args, stream) on device `index`'s current stream, with that device current."""
+    torch = _torch()
+    handle = torch.cuda.current_stream(index).cuda_stream
     if torch.cuda.current_device() == index:
         status = fn(*args, handle)
     else:
@@ -429,7 +440,10 @@ def q4_linear(x, packed, bias=None, activation="none", gated=False, residual=Non
     x [m, k] fp32, fp16 or bf16; packed [n, k/32*18] uint8; bias [n]; residual of
     y's shape and dtype (it may be y itself).  activation: none, relu, gelu (tanh
     form), gelu_erf or silu.  y defaults to x's dtype."""
-    if y is None and y_dtype is None and workspace is None and stream is None:
+    if stream is not None:
+        with _on(stream, x):
+            return q4_linear(x, packed, bias, activation, gated, residual, y, y_dtype, workspace)
+    if y is None and y_dtype is None and workspace is None:
         fast = _FAST or _fast()
         if fast is not None:
             out = fast.linear(x, packed, bias, ACTIVATIONS.get(activation), gated, residual)
@@ -447,7 +461,7 @@ def q4_linear(x, packed, bias=None, activation="none", gated=False, residual=Non
     L = lib()
     workspace, wptr, wbytes = _workspace(
         workspace, L.q4_linear_workspace_size(m, n, k, xd, ep.gated), x.device)
-    _launch(index, stream, "q4_linear", L.q4_linear, x.data_ptr(), xd, packed.data_ptr(),
+    _launch(index, "q4_linear", L.q4_linear, x.data_ptr(), xd, packed.data_ptr(),
             ctypes.byref(ep), y.data_ptr(), _dtype_code(y), m, n, k, wptr, wbytes)
     return y
 
@@ -515,7 +529,11 @@ def q4_route(logits, topk, score="softmax", bias=None, groups=1, group_topk=1, g
     weights [m, topk] fp32, plan); ties go to the lowest index, an expert with a
     logit of -inf or NaN is not chosen, and a place without an expert is id -1,
     weight 0."""
-    if ids is None and weights is None and stream is None:
+    if stream is not None:
+        with _on(stream, logits):
+            return q4_route(logits, topk, score, bias, groups, group_topk, group_score, renormalise, scale, ids,
+                            weights)
+    if ids is None and weights is None:
         fast = _FAST or _fast()
         if fast is not None:
             out = fast.route(logits, topk, bias, SCORES.get(score), groups, group_topk,
@@ -531,26 +549,28 @@ def q4_route(logits, topk, score="softmax", bias=None, groups=1, group_topk=1, g
     plan = _new_plan(m, topk, experts, logits.device)
     ids = _ids_out(ids, (m, topk), torch.int32, logits.device, "ids")
     weights = _ids_out(weights, (m, topk), torch.float32, logits.device, "weights")
-    _launch(index, stream, "q4_route", lib().q4_route, logits.data_ptr(), _dtype_code(logits), m, experts,
+    _launch(index, "q4_route", lib().q4_route, logits.data_ptr(), _dtype_code(logits), m, experts,
             topk, ctypes.byref(r), ids.data_ptr(), weights.data_ptr(), plan.words.data_ptr())
     return ids, weights, plan
 
 
 def q4_route_plan(ids, experts, stream=None):
     """The plan of given ids [m, topk] int32; ids outside 0 .. experts - 1 name no expert."""
-    if stream is None:
-        fast = _FAST or _fast()
-        if fast is not None:
-            words = fast.route_plan(ids, experts)
-            if words is not None:
-                return Plan(words, ids.shape[0], ids.shape[1], experts)
+    if stream is not None:
+        with _on(stream, ids):
+            return q4_route_plan(ids, experts)
+    fast = _FAST or _fast()
+    if fast is not None:
+        words = fast.route_plan(ids, experts)
+        if words is not None:
+            return Plan(words, ids.shape[0], ids.shape[1], experts)
     torch = _torch()
     index = _same_device(ids)
     if ids.dtype != torch.int32 or ids.dim() != 2:
         raise ValueError(f"ids must be int32 [m, topk]; got {ids.dtype} {tuple(ids.shape)}")
     m, topk = int(ids.shape[0]), int(ids.shape[1])
     plan = _new_plan(m, topk, int(experts), ids.device)
-    _launch(index, stream, "q4_route_plan", lib().q4_route_plan, ids.data_ptr(), m, topk, int(experts),
+    _launch(index, "q4_route_plan", lib().q4_route_plan, ids.data_ptr(), m, topk, int(experts),
             plan.words.data_ptr())
     return plan
 
@@ -579,7 +599,10 @@ def q4_experts(x, packed, plan, bias=None, activation="none", gated=False, weigh
     is [m * topk, nout], and rows of pairs without an expert are left as they
     were (not written); with weights [m, topk] fp32 y is [m, nout], the weighted
     sum over a token's experts.  The residual has y's shape and dtype."""
-    if y is None and y_dtype is None and workspace is None and stream is None:
+    if stream is not None:
+        with _on(stream, x):
+            return q4_experts(x, packed, plan, bias, activation, gated, weights, residual, y, y_dtype, workspace)
+    if y is None and y_dtype is None and workspace is None:
         fast = _FAST or _fast()
         if fast is not None:
             out = fast.experts(x, packed, plan.words, plan.m, plan.topk, plan.experts, bias,
@@ -606,7 +629,7 @@ def q4_experts(x, packed, plan, bias=None, activation="none", gated=False, weigh
     workspace, wptr, wbytes = _workspace(
         workspace, L.q4_experts_workspace_size(m, topk, experts, n, k, x_rows, xd, ep.gated,
                                                0 if weights is None else 1), x.device)
-    _launch(index, stream, "q4_experts", L.q4_experts, x.data_ptr(), xd, x_rows, packed.data_ptr(),
+    _launch(index, "q4_experts", L.q4_experts, x.data_ptr(), xd, x_rows, packed.data_ptr(),
             ctypes.byref(ep), plan.words.data_ptr(), None if weights is None else weights.data_ptr(),
             y.data_ptr(), _dtype_code(y), m, topk, experts, n, k, wptr, wbytes)
     return y
@@ -628,8 +651,12 @@ def q4_moe(x, logits, up, down, topk, activation="silu", gated=True, up_bias=Non
     and add the rows up by the routing weights, plus the residual.  The rows between
     the products have x's dtype.  Routing options as in q4_route; ids and weights
     receive the routing if given."""
-    if (y is None and y_dtype is None and workspace is None and stream is None and ids is None
-            and weights is None):
+    if stream is not None:
+        with _on(stream, x):
+            return q4_moe(x, logits, up, down, topk, activation, gated, up_bias, down_bias, residual, score,
+                          route_bias, groups, group_topk, group_score, renormalise, scale, ids, weights, y,
+                          y_dtype, workspace)
+    if y is None and y_dtype is None and workspace is None and ids is None and weights is None:
         fast = _FAST or _fast()
         if fast is not None:
             out = fast.moe(x, logits, up, down, topk, ACTIVATIONS.get(activation), gated, up_bias,
@@ -665,7 +692,7 @@ def q4_moe(x, logits, up, down, topk, activation="silu", gated=True, up_bias=Non
     L = lib()
     workspace, wptr, wbytes = _workspace(
         workspace, L.q4_moe_workspace_size(m, topk, experts, hidden, inter, xd, up_ep.gated), x.device)
-    _launch(index, stream, "q4_moe", L.q4_moe, x.data_ptr(), xd, logits.data_ptr(), _dtype_code(logits),
+    _launch(index, "q4_moe", L.q4_moe, x.data_ptr(), xd, logits.data_ptr(), _dtype_code(logits),
             ctypes.byref(r), up.data_ptr(), ctypes.byref(up_ep), down.data_ptr(), ctypes.byref(down_ep),
             y.data_ptr(), _dtype_code(y), m, topk, experts, hidden, inter,
             None if ids is None else ids.data_ptr(), None if weights is None else weights.data_ptr(), wptr,
