@@ -20,31 +20,76 @@ constexpr int kMaxExperts = 1024;
 constexpr int kOneTokens = 16;  // most tokens of a single-workgroup routing,
 constexpr int kOnePerLane = 4;  // and most experts per lane (its waves' LDS)
 
-// Lane j's choice as the j-th of token t; hist: counts, or nullptr.
+// Lane j's choice as the j-th of token t.
 __device__ __forceinline__ void write_choice(const Choice& c, int64_t t, const RouteParams& a, int* ids,
-                                             float* weights, int* hist) {
+                                             float* weights) {
   const int lane = threadIdx.x & (kWave - 1);
   if (lane >= a.topk) return;
   ids[t * a.topk + lane] = c.id;
   weights[t * a.topk + lane] = c.weight;
-  if (hist != nullptr) atomicAdd(&hist[c.id < 0 ? a.experts : c.id], 1);
 }
 
 // ------------------------------------------------------------------ plan
 
 struct PlanLds {
-  int total[kMaxExperts + 1];  // pairs per expert; the last entry: without one
-  int base[kMaxExperts + 1];   // next place of an expert's pairs
-  int tile0[kMaxExperts];      // first tile
+  int base[kMaxExperts + 1];  // next place of an expert's pairs; at the end: of those without one
+  int tile0[kMaxExperts];     // first tile
   int wave_pairs[kWaves], wave_tiles[kWaves];
-  alignas(16) int ids[kThreads];
+  int ids[kThreads];
+  uint16_t count[kWaves][kMaxExperts + 1];  // pairs per wavefront and expert (the last entry: without one)
 };
 
-// Offsets (into base[]) and first tiles from the totals: thread e scans expert e.
-__device__ __forceinline__ void scan_experts(PlanLds& s, int experts, int tile_rows) {
+// Clears the counts of `pairs` pairs; plan_one's first barrier is behind it.
+__device__ __forceinline__ void clear_counts(PlanLds& s, int pairs, int experts) {
+  const int waves = (pairs + kWave - 1) / kWave;
+  for (int w = 0; w < waves; ++w)
+    for (int e = threadIdx.x; e <= experts; e += kThreads) s.count[w][e] = 0;
+}
+
+// Tile i of expert e, which has c pairs from place `first` on.
+__device__ __forceinline__ void write_tile(int e, int i, int first, int c, int tile0, const PlanLayout& L,
+                                           int* plan) {
+  const int left = c - i * L.tile_rows;
+  *reinterpret_cast<int4*>(plan + L.tiles + static_cast<int64_t>(tile0 + i) * L.rec_words) =
+      int4{e, first + i * L.tile_rows, left < L.tile_rows ? left : L.tile_rows, 0};
+}
+
+// Pair p is the r-th of its expert, whose places start at `first` and whose
+// tiles at tile0.
+__device__ __forceinline__ void place_pair(int p, int r, int first, int tile0, const PlanLayout& L,
+                                           int* plan) {
+  plan[L.order + first + r] = p;
+  plan[L.pos + p] = first + r;
+  const int t = r / L.tile_rows;
+  plan[L.tiles + static_cast<int64_t>(tile0 + t) * L.rec_words + 4 + (r - t * L.tile_rows)] = p;
+}
+
+// The whole plan of at most kThreads pairs by one workgroup, one pair per
+// thread.  Their ids are in s.ids (`experts` for a pair without one), the counts
+// cleared.  A pair's rank among its expert's is the count of the earlier
+// wavefronts and of the earlier lanes.  Nothing goes to memory before the last
+// barrier, which would wait for it.
+__device__ __forceinline__ void plan_one(PlanLds& s, int pairs, int experts, const PlanLayout& L, int* plan) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  const int c = tid < experts ? s.total[tid] : 0;
-  const int tc = (c + tile_rows - 1) / tile_rows;
+  const int waves = (pairs + kWave - 1) / kWave;
+  __syncthreads();
+  const int id = tid < pairs ? s.ids[tid] : -1;  // (-1 matches no pair)
+  // Lanes of this wavefront with the same id: agreement in every bit of id + 1.
+  uint64_t same = ~uint64_t{0};
+#pragma unroll
+  for (int b = 0; b < 11; ++b) {  // (id + 1 <= kMaxExperts + 1 < 2^11)
+    const bool set = (((id + 1) >> b) & 1) != 0;
+    const uint64_t who = __ballot(set);
+    same &= set ? who : ~who;
+  }
+  int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
+  if (id >= 0 && rank == 0) s.count[wave][id] = static_cast<uint16_t>(__popcll(same));
+  __syncthreads();
+  // Thread e: expert e's pairs and tiles, and those of the experts before it.
+  int c = 0;
+  if (tid < experts)
+    for (int w = 0; w < waves; ++w) c += s.count[w][tid];
+  const int tc = (c + L.tile_rows - 1) / L.tile_rows;
   int p = c, t = tc;  // inclusive sums over the wave
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
@@ -58,6 +103,8 @@ __device__ __forceinline__ void scan_experts(PlanLds& s, int experts, int tile_r
     s.wave_pairs[wave] = p;
     s.wave_tiles[wave] = t;
   }
+  if (id >= 0)
+    for (int w = 0; w < wave; ++w) rank += s.count[w][id];
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
@@ -73,65 +120,16 @@ __device__ __forceinline__ void scan_experts(PlanLds& s, int experts, int tile_r
     if (tid == experts - 1) s.base[experts] = p;
   }
   __syncthreads();
-}
-
-// Tiles of expert e (c pairs from place `first`), written by one wavefront.
-__device__ __forceinline__ void write_tiles(int e, int first, int c, int tile0, const PlanLayout& L,
-                                            int* plan) {
-  for (int i = threadIdx.x & (kWave - 1); i * L.tile_rows < c; i += kWave) {
-    const int left = c - i * L.tile_rows;
-    *reinterpret_cast<int4*>(plan + L.tiles + static_cast<int64_t>(tile0 + i) * L.rec_words) =
-        int4{e, first + i * L.tile_rows, left < L.tile_rows ? left : L.tile_rows, 0};
-  }
-}
-
-// Pair p is the r-th of its expert, whose places start at `first` and whose
-// tiles at tile0.
-__device__ __forceinline__ void place_pair(int p, int r, int first, int tile0, const PlanLayout& L,
-                                           int* plan) {
-  plan[L.order + first + r] = p;
-  plan[L.pos + p] = first + r;
-  const int t = r / L.tile_rows;
-  plan[L.tiles + static_cast<int64_t>(tile0 + t) * L.rec_words + 4 + (r - t * L.tile_rows)] = p;
-}
-
-// The whole plan of at most kThreads pairs whose counts are in s.total, by one
-// workgroup.
-__device__ __forceinline__ void plan_one(PlanLds& s, const int* ids, int pairs, int experts,
-                                         const PlanLayout& L, int* plan) {
-  const int tid = threadIdx.x, wave = tid / kWave;
-  scan_experts(s, experts, L.tile_rows);
-  if (tid <= experts) plan[tid] = s.base[tid];
-  if (experts == kThreads && tid == 0) plan[experts] = s.base[experts];
-  if (tid == 0) {
-    plan[L.head] = s.tile0[experts - 1] + (s.total[experts - 1] + L.tile_rows - 1) / L.tile_rows;
-    plan[L.head + 1] = L.tile_rows;
-  }
-  for (int e = wave; e < experts; e += kWaves) write_tiles(e, s.base[e], s.total[e], s.tile0[e], L, plan);
-  int id = -1;  // (behind the end: matches no pair)
-  if (tid < pairs) {
-    id = ids[tid];
-    if (id < 0 || id >= experts) id = experts;
-  }
-  s.ids[tid] = id;
-  // Lanes of this wavefront with the same id: agreement in every bit of id + 1.
-  uint64_t same = ~uint64_t{0};
-#pragma unroll
-  for (int b = 0; b < 11; ++b) {  // (id + 1 <= kMaxExperts + 1 < 2^11)
-    const bool set = (((id + 1) >> b) & 1) != 0;
-    const uint64_t who = __ballot(set);
-    same &= set ? who : ~who;
-  }
-  __syncthreads();
-  if (id >= 0) {
-    int rank = 0;  // earlier pairs of the same expert
-    const int4* v4 = reinterpret_cast<const int4*>(s.ids);
-#pragma unroll 4
-    for (int j = 0; j < wave * (kWave / 4); ++j) {
-      const int4 v = v4[j];
-      rank += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
+  if (tid < experts) {
+    plan[tid] = p - c;
+    for (int i = 0; i < tc; ++i) write_tile(tid, i, p - c, c, t - tc, L, plan);
+    if (tid == experts - 1) {
+      plan[experts] = p;
+      plan[L.head] = t;
+      plan[L.head + 1] = L.tile_rows;
     }
-    rank += __popcll(same & ((uint64_t{1} << (tid & (kWave - 1))) - 1));
+  }
+  if (id >= 0) {
     if (id < experts) {
       place_pair(tid, rank, s.base[id], s.tile0[id], L, plan);
     } else {
@@ -149,15 +147,16 @@ __global__ __launch_bounds__(kThreads) void route_one_kernel(const void* __restr
   __shared__ PlanLds s;
   __shared__ double scores[sizeof(K) == 8 ? kWaves : 1][NPL * kWave];
   __shared__ K keys[kWaves][NPL * kWave];
-  const int tid = threadIdx.x, wave = tid / kWave;
-  for (int e = tid; e <= a.experts; e += kThreads) s.total[e] = 0;
-  __syncthreads();
-  for (int t = wave; t < m; t += kWaves)
-    write_choice(route_token<NPL, K>(logits, dt, t, a, scores[sizeof(K) == 8 ? wave : 0], keys[wave]), t, a,
-                 ids, weights, s.total);
-  if (plan == nullptr) return;
-  __syncthreads();
-  plan_one(s, ids, m * a.topk, a.experts, L, plan);
+  const int tid = threadIdx.x, wave = tid / kWave, lane = tid & (kWave - 1);
+  if (plan != nullptr) clear_counts(s, m * a.topk, a.experts);
+  static_assert(kOneTokens <= kWaves, "one token per wavefront");
+  Choice c{-1, 0.0f};
+  if (wave < m) {
+    c = route_token<NPL, K>(logits, dt, wave, a, scores[sizeof(K) == 8 ? wave : 0], keys[wave]);
+    if (lane < a.topk) s.ids[wave * a.topk + lane] = c.id < 0 ? a.experts : c.id;
+  }
+  if (plan != nullptr) plan_one(s, m * a.topk, a.experts, L, plan);
+  if (wave < m) write_choice(c, wave, a, ids, weights);
 }
 
 // Choice, one token per wavefront.
@@ -172,7 +171,7 @@ __global__ __launch_bounds__(4 * kWave) void route_kernel(const void* __restrict
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave;
   if (t < m)
     write_choice(route_token<NPL, K>(logits, dt, t, a, scores[sizeof(K) == 8 ? wave : 0], keys[wave]), t, a,
-                 ids, weights, nullptr);
+                 ids, weights);
 }
 
 // The plan of given ids by one workgroup (at most kThreads pairs).
@@ -181,14 +180,12 @@ __global__ __launch_bounds__(kThreads) void plan_one_kernel(const int* __restric
                                                             int* __restrict__ plan) {
   __shared__ PlanLds s;
   const int tid = threadIdx.x;
-  for (int e = tid; e <= experts; e += kThreads) s.total[e] = 0;
-  __syncthreads();
   if (tid < pairs) {
     const int id = ids[tid];
-    atomicAdd(&s.total[id < 0 || id >= experts ? experts : id], 1);
+    s.ids[tid] = id < 0 || id >= experts ? experts : id;
   }
-  __syncthreads();
-  plan_one(s, ids, pairs, experts, L, plan);
+  clear_counts(s, pairs, experts);
+  plan_one(s, pairs, experts, L, plan);
 }
 
 // Workgroup e < experts places expert e's pairs, workgroup `experts` what is
@@ -266,7 +263,8 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(const int* __restrict__ 
       plan[L.head + 1] = L.tile_rows;
     }
   }
-  if (!rest && wave == 0) write_tiles(me, first, count, tile0, L, plan);
+  if (!rest && wave == 0)
+    for (int i = lane; i * L.tile_rows < count; i += kWave) write_tile(me, i, first, count, tile0, L, plan);
   int at = before;
   for (int c0 = 0; c0 < chunks; c0 += kAhead) {
     int id[kAhead];
