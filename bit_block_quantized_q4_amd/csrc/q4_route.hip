@@ -2,10 +2,10 @@
 //
 // Choice: one wavefront per token, see q4_route_token.hpp.
 //
-// Plan: a stable counting sort of the pairs by expert.  One workgroup per
-// expert counts the earlier experts' pairs in an LDS histogram (integer adds:
-// their order does not matter) and places its own in ascending order by
-// ballots.  Up to 16 tokens run as one workgroup and one launch.
+// Plan: a stable counting sort of the pairs by expert, in one launch: every
+// workgroup counts all pairs in LDS (integer adds: their order does not matter)
+// and places its own, ranked by ballots.  Up to 16 tokens run as one workgroup
+// and one launch with their choice.
 //
 // Bound by latency and by the instructions of the choice: 4096 tokens of 256
 // experts are 2 MB of logits (0.4 us at 5 TB/s) and 0.6 MB of outputs.
@@ -46,6 +46,56 @@ __device__ __forceinline__ void clear_counts(PlanLds& s, int pairs, int experts)
     for (int e = threadIdx.x; e <= experts; e += kThreads) s.count[w][e] = 0;
 }
 
+// The earlier lanes of this wavefront with the same id (-1: none); its count by
+// their first lane into s.count.
+__device__ __forceinline__ int rank_in_wave(PlanLds& s, int id) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  uint64_t same = ~uint64_t{0};  // agreement in every bit of id + 1
+#pragma unroll
+  for (int b = 0; b < 11; ++b) {  // (id + 1 <= kMaxExperts + 1 < 2^11)
+    const bool set = (((id + 1) >> b) & 1) != 0;
+    const uint64_t who = __ballot(set);
+    same &= set ? who : ~who;
+  }
+  const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
+  if (id >= 0 && rank == 0) s.count[wave][id] = static_cast<uint16_t>(__popcll(same));
+  return rank;
+}
+
+// Thread e < experts has expert e's pairs c and tiles tc, also in p and t; these
+// become the sums up to and with e.  First places and tiles into s, behind a
+// barrier.
+__device__ __forceinline__ void scan_experts(PlanLds& s, int experts, int c, int tc, int& p, int& t) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int op = __shfl_up(p, off), ot = __shfl_up(t, off);
+    if (lane >= off) {
+      p += op;
+      t += ot;
+    }
+  }
+  if (lane == kWave - 1) {
+    s.wave_pairs[wave] = p;
+    s.wave_tiles[wave] = t;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const int op = s.wave_pairs[w], ot = s.wave_tiles[w];
+    if (w < wave) {
+      p += op;
+      t += ot;
+    }
+  }
+  if (tid < experts) {
+    s.base[tid] = p - c;
+    s.tile0[tid] = t - tc;
+    if (tid == experts - 1) s.base[experts] = p;
+  }
+  __syncthreads();
+}
+
 // Tile i of expert e, which has c pairs from place `first` on.
 __device__ __forceinline__ void write_tile(int e, int i, int first, int c, int tile0, const PlanLayout& L,
                                            int* plan) {
@@ -70,56 +120,20 @@ __device__ __forceinline__ void place_pair(int p, int r, int first, int tile0, c
 // wavefronts and of the earlier lanes.  Nothing goes to memory before the last
 // barrier, which would wait for it.
 __device__ __forceinline__ void plan_one(PlanLds& s, int pairs, int experts, const PlanLayout& L, int* plan) {
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int tid = threadIdx.x, wave = tid / kWave;
   const int waves = (pairs + kWave - 1) / kWave;
   __syncthreads();
   const int id = tid < pairs ? s.ids[tid] : -1;  // (-1 matches no pair)
-  // Lanes of this wavefront with the same id: agreement in every bit of id + 1.
-  uint64_t same = ~uint64_t{0};
-#pragma unroll
-  for (int b = 0; b < 11; ++b) {  // (id + 1 <= kMaxExperts + 1 < 2^11)
-    const bool set = (((id + 1) >> b) & 1) != 0;
-    const uint64_t who = __ballot(set);
-    same &= set ? who : ~who;
-  }
-  int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
-  if (id >= 0 && rank == 0) s.count[wave][id] = static_cast<uint16_t>(__popcll(same));
+  int rank = rank_in_wave(s, id);
   __syncthreads();
-  // Thread e: expert e's pairs and tiles, and those of the experts before it.
   int c = 0;
   if (tid < experts)
     for (int w = 0; w < waves; ++w) c += s.count[w][tid];
-  const int tc = (c + L.tile_rows - 1) / L.tile_rows;
-  int p = c, t = tc;  // inclusive sums over the wave
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const int op = __shfl_up(p, off), ot = __shfl_up(t, off);
-    if (lane >= off) {
-      p += op;
-      t += ot;
-    }
-  }
-  if (lane == kWave - 1) {
-    s.wave_pairs[wave] = p;
-    s.wave_tiles[wave] = t;
-  }
   if (id >= 0)
     for (int w = 0; w < wave; ++w) rank += s.count[w][id];
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const int op = s.wave_pairs[w], ot = s.wave_tiles[w];
-    if (w < wave) {
-      p += op;
-      t += ot;
-    }
-  }
-  if (tid < experts) {
-    s.base[tid] = p - c;
-    s.tile0[tid] = t - tc;
-    if (tid == experts - 1) s.base[experts] = p;
-  }
-  __syncthreads();
+  const int tc = (c + L.tile_rows - 1) / L.tile_rows;
+  int p = c, t = tc;
+  scan_experts(s, experts, c, tc, p, t);
   if (tid < experts) {
     plan[tid] = p - c;
     for (int i = 0; i < tc; ++i) write_tile(tid, i, p - c, c, t - tc, L, plan);
@@ -188,102 +202,95 @@ __global__ __launch_bounds__(kThreads) void plan_one_kernel(const int* __restric
   plan_one(s, pairs, experts, L, plan);
 }
 
-// Workgroup e < experts places expert e's pairs, workgroup `experts` what is
-// left: the order behind the last pair, the pairs without an expert, the totals.
-// Wavefront w takes the w-th sixteenth of the ids, 64 at a time: the earlier
-// experts' counts go into an LDS histogram (their tiles come before its own,
-// without gaps: tile slots left empty between the experts' cost the products a
-// quarter of their time), its own are counted and placed by ballots.
+// Workgroup g places the pairs g span .. (g + 1) span - 1, after counting all
+// pairs by expert, those before its own apart: integer adds in LDS, four copies
+// by lane so that pairs of one expert meet less often, 32 ids per thread in
+// flight.  (Tiles are numbered without gaps: slots left empty between the experts'
+// cost the products a quarter of their time.)  32768 pairs of 256 experts: 8.0
+// us; with a workgroup per expert that placed that expert's pairs, 17.0.
+constexpr int kCopies = 4, kQuads = 8;
 __global__ __launch_bounds__(kThreads) void plan_kernel(const int* __restrict__ ids, int pairs, int experts,
-                                                        PlanLayout L, int* __restrict__ plan) {
-  __shared__ int hist[kMaxExperts + 1];
-  __shared__ int mine_s[kWaves], first_s, tile_s;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  const int me = blockIdx.x;
-  for (int e = tid; e < me; e += kThreads) hist[e] = 0;
+                                                        int span, PlanLayout L, int* __restrict__ plan) {
+  __shared__ PlanLds s;
+  __shared__ int hist[2][kCopies][kMaxExperts + 1];  // before this workgroup's pairs, and from them on
+  __shared__ int before[kMaxExperts + 1];
+  const int tid = threadIdx.x, wave = tid / kWave;
+  const int begin = blockIdx.x * span;
+  const int end = pairs - begin < span ? pairs : begin + span;
+  for (int e = tid; e <= experts; e += kThreads)
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) hist[0][i][e] = hist[1][i][e] = 0;
   __syncthreads();
-  const int chunks = (pairs + kThreads - 1) / kThreads;
-  const int p0 = wave * chunks * kWave;
-  constexpr int kAhead = 8;  // loads in flight
-  // Ids of chunks c0 .. c0 + 7; experts + 1 (which counts nowhere) past the end.
-  auto load = [&](int c0, int (&id)[kAhead]) {
+  auto expert = [&](int id) { return id < 0 || id >= experts ? experts : id; };
+  auto add = [&](int p, int id) { atomicAdd(&hist[p < begin ? 0 : 1][tid % kCopies][expert(id)], 1); };
+  const int quads = pairs / 4;
+  for (int q0 = 0; q0 < quads; q0 += kThreads * kQuads) {
+    int4 v[kQuads];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int p = p0 + (c0 + u) * kWave + lane;
-      id[u] = ids[p < pairs ? p : pairs - 1];
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const bool in = c0 + u < chunks && p0 + (c0 + u) * kWave + lane < pairs;
-      id[u] = !in ? experts + 1 : id[u] < 0 || id[u] >= experts ? experts : id[u];
-    }
-  };
-  int mine = 0;
-  for (int c0 = 0; c0 < chunks; c0 += kAhead) {
-    int id[kAhead];
-    load(c0, id);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      mine += __popcll(__ballot(id[u] == me));
-      if (id[u] < me) atomicAdd(&hist[id[u]], 1);
-    }
-  }
-  if (lane == 0) mine_s[wave] = mine;
-  __syncthreads();
-  if (wave == 0) {
-    int f = 0, t = 0;
-    for (int e = lane; e < me; e += kWave) {
-      f += hist[e];
-      t += (hist[e] + L.tile_rows - 1) / L.tile_rows;
+    for (int u = 0; u < kQuads; ++u) {
+      const int q = q0 + u * kThreads + tid;
+      v[u] = reinterpret_cast<const int4*>(ids)[q < quads ? q : quads - 1];
     }
 #pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      f += __shfl_xor(f, off);
-      t += __shfl_xor(t, off);
-    }
-    if (lane == 0) {
-      first_s = f;
-      tile_s = t;
-    }
-  }
-  __syncthreads();
-  const int first = first_s, tile0 = tile_s;
-  int count = 0, before = 0;  // before: in the earlier wavefronts' shares
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const int n = mine_s[w];
-    count += n;
-    if (w < wave) before += n;
-  }
-  const bool rest = me == experts;
-  if (tid == 0) {
-    plan[me] = first;
-    if (rest) {
-      plan[L.head] = tile0;
-      plan[L.head + 1] = L.tile_rows;
-    }
-  }
-  if (!rest && wave == 0)
-    for (int i = lane; i * L.tile_rows < count; i += kWave) write_tile(me, i, first, count, tile0, L, plan);
-  int at = before;
-  for (int c0 = 0; c0 < chunks; c0 += kAhead) {
-    int id[kAhead];
-    load(c0, id);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const uint64_t mask = __ballot(id[u] == me);
-      if (id[u] == me) {
-        const int p = p0 + (c0 + u) * kWave + lane;
-        const int r = at + __popcll(mask & ((uint64_t{1} << lane) - 1));
-        if (rest) {
-          plan[L.order + first + r] = -1;
-          plan[L.pos + p] = -1;
-        } else {
-          place_pair(p, r, first, tile0, L, plan);
-        }
+    for (int u = 0; u < kQuads; ++u) {
+      const int q = q0 + u * kThreads + tid;
+      if (q < quads) {
+        add(4 * q, v[u].x);
+        add(4 * q, v[u].y);
+        add(4 * q, v[u].z);
+        add(4 * q, v[u].w);
       }
-      at += __popcll(mask);
     }
+  }
+  if (tid < pairs - 4 * quads) add(4 * quads + tid, ids[4 * quads + tid]);
+  __syncthreads();
+  int c = 0;
+  for (int e = tid; e <= experts; e += kThreads) {
+    int b = 0, n = 0;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      b += hist[0][i][e];
+      n += hist[1][i][e];
+    }
+    before[e] = b;
+    if (e == tid && e < experts) c = b + n;
+  }
+  const int tc = (c + L.tile_rows - 1) / L.tile_rows;
+  int p = c, t = tc;
+  scan_experts(s, experts, c, tc, p, t);
+  if (tid < experts) {
+    for (int i = blockIdx.x; i < tc; i += gridDim.x) write_tile(tid, i, p - c, c, t - tc, L, plan);
+    if (blockIdx.x == 0) {
+      plan[tid] = p - c;
+      if (tid == experts - 1) {
+        plan[experts] = p;
+        plan[L.head] = t;
+        plan[L.head + 1] = L.tile_rows;
+      }
+    }
+  }
+  for (int p0 = begin; p0 < end; p0 += kThreads) {
+    const int at = p0 + tid;
+    const int id = at < end ? expert(ids[at]) : -1;
+    clear_counts(s, kThreads, experts);
+    __syncthreads();
+    int rank = rank_in_wave(s, id);
+    __syncthreads();
+    if (id >= 0) {
+      for (int w = 0; w < wave; ++w) rank += s.count[w][id];
+      rank += before[id];
+      if (id < experts) {
+        place_pair(at, rank, s.base[id], s.tile0[id], L, plan);
+      } else {
+        plan[L.order + s.base[id] + rank] = -1;
+        plan[L.pos + at] = -1;
+      }
+    }
+    if (p0 + kThreads >= end) break;
+    __syncthreads();
+    for (int e = tid; e <= experts; e += kThreads)
+      for (int w = 0; w < kWaves; ++w) before[e] += s.count[w][e];
+    __syncthreads();
   }
 }
 
@@ -335,8 +342,11 @@ hipError_t launch_route_plan(const int* ids, int64_t m, int64_t topk, int64_t ex
   void* argv[] = {&ids, &pairs, &ne, &L, &plan};
   if (pairs <= kThreads)
     return hipLaunchKernel(reinterpret_cast<const void*>(&plan_one_kernel), dim3(1), dim3(kThreads), argv, 0, s);
-  return hipLaunchKernel(reinterpret_cast<const void*>(&plan_kernel), dim3(static_cast<unsigned>(experts + 1)),
-                         dim3(kThreads), argv, 0, s);
+  // A workgroup per 1024 pairs, up to one per compute unit (each reads all ids).
+  const int64_t chunks = (m * topk + kThreads - 1) / kThreads, cu = device_cu_count();
+  int span = static_cast<int>((chunks + cu - 1) / cu) * kThreads;
+  void* argl[] = {&ids, &pairs, &ne, &span, &L, &plan};
+  return launch_blocks(reinterpret_cast<const void*>(&plan_kernel), (pairs + span - 1) / span, kThreads, argl, 0, s);
 }
 
 }  // namespace q4

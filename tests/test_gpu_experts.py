@@ -191,3 +191,23 @@ def test_experts_named_often_by_a_token(q4lib, gpu, m, topk, E, n, k, xt):
     ids[m // 2] = torch.arange(topk, dtype=torch.int32)
     run_experts(q4lib, gpu, m, topk, E, n, k, xt, gated=True, act="silu", ids=ids, seed=m)
     run_experts(q4lib, gpu, m, topk, E, n, k, xt, combine=True, residual=True, ids=ids, seed=m)
+
+
+@pytest.mark.parametrize("m,topk,experts", [(1025, 1, 3), (257, 4, 1), (1366, 3, 7), (2000, 8, 1024), (300001, 1, 64),
+                                            (70000, 8, 200)])
+@pytest.mark.parametrize("skew", [False, True])
+def test_plan_of_many_pairs(q4lib, gpu, m, topk, experts, skew):
+    """Any number of workgroups and of pairs per workgroup, odd ends, nearly all
+    pairs on one expert; against a stable sort."""
+    g = torch.Generator().manual_seed(m)
+    ids = torch.randint(-2, experts + 2, (m, topk), generator=g, dtype=torch.int32)
+    if skew:
+        ids[torch.rand((m, topk), generator=g) < 0.9] = experts // 2
+    plan = q4lib.q4_route_plan(ids.to(gpu), experts)
+    key = torch.where((ids < 0) | (ids >= experts), experts, ids).flatten()
+    counts = torch.bincount(key, minlength=experts + 1)[:experts]
+    offsets = torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)])
+    order = torch.sort(key, dim=0, stable=True).indices
+    order[offsets[-1]:] = -1
+    assert torch.equal(plan.offsets.cpu().long(), offsets)
+    assert torch.equal(plan.order.cpu().long(), order)
