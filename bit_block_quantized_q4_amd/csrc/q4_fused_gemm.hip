@@ -319,40 +319,69 @@ __global__ __launch_bounds__(256) void fused_reduce_kernel(FusedArgs a, int spli
     if (out0 + c + i < nout) finish_store(a.ep, 0, r, out0 + c + i, s0[i], s1[i]);
 }
 
-// bf16 rows -> fp16 rows and the inverse of their power-of-two factors; one
-// workgroup per row.  The sums of a row with an infinity or a NaN are not
+// bf16 rows -> fp16 rows and the inverse of their power-of-two factors.  WIDE:
+// one workgroup per row, read twice; else one wavefront per row of at most
+// kStagePieces x 64 16-byte pieces, which stay in registers (16384 rows of 768:
+// 13.2 us against 16.9).  The sums of a row with an infinity or a NaN are not
 // finite, so its tiles take the exact route.
+constexpr int kStagePieces = 4;
+template <bool WIDE>
 __global__ __launch_bounds__(256) void stage_bf16_kernel(const uint16_t* __restrict__ x,
                                                          uint16_t* __restrict__ out,
-                                                         float* __restrict__ inv, int64_t k) {
-  __shared__ uint32_t top_s[4];
-  const int64_t row = blockIdx.x;
+                                                         float* __restrict__ inv, int64_t rows, int64_t k) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int64_t row = WIDE ? blockIdx.x : blockIdx.x * int64_t{4} + wave;
+  if (row >= rows) return;  // whole wavefront (WIDE: none)
   const u32x4* src = reinterpret_cast<const u32x4*>(x + row * k);
   u32x4* dst = reinterpret_cast<u32x4*>(out + row * k);
   const int64_t np = k / 8;
   uint32_t top = 0;  // largest magnitude, as bf16 bits
-  for (int64_t p = threadIdx.x; p < np; p += 256) {
-    const u32x4 v = src[p];
+  auto look = [&](const u32x4& v) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) top = max_magnitude_bf16(top, v[e]);
-  }
+  };
+  auto over_wave = [&]() {
 #pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const uint32_t o = __shfl_xor(top, off);
-    top = o > top ? o : top;
-  }
-  if ((threadIdx.x & 63) == 0) top_s[threadIdx.x >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 4; ++w) top = top_s[w] > top ? top_s[w] : top;
-  const int shift = bf16_row_shift(top);
-  const float f = power_of_two(shift);
-  if (threadIdx.x == 0) inv[row] = power_of_two(-shift);
-  for (int64_t p = threadIdx.x; p < np; p += 256) {
-    u32x4 v = src[p];
+    for (int off = 1; off < kWave; off <<= 1) {
+      const uint32_t o = __shfl_xor(top, off);
+      top = o > top ? o : top;
+    }
+  };
+  auto put = [&](int64_t p, u32x4 v, float f) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = bf16x2_scaled_to_f16x2(v[e], f);
     dst[p] = v;
+  };
+  if constexpr (WIDE) {
+    __shared__ uint32_t top_s[4];
+    for (int64_t p = threadIdx.x; p < np; p += 256) look(src[p]);
+    over_wave();
+    if (lane == 0) top_s[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = top_s[w] > top ? top_s[w] : top;
+    const int shift = bf16_row_shift(top);
+    const float f = power_of_two(shift);
+    if (threadIdx.x == 0) inv[row] = power_of_two(-shift);
+    for (int64_t p = threadIdx.x; p < np; p += 256) put(p, src[p], f);
+  } else {
+    u32x4 v[kStagePieces];
+#pragma unroll
+    for (int i = 0; i < kStagePieces; ++i) {
+      const int64_t p = lane + i * kWave;
+      v[i] = src[p < np ? p : np - 1];
+    }
+#pragma unroll
+    for (int i = 0; i < kStagePieces; ++i) look(v[i]);
+    over_wave();
+    const int shift = bf16_row_shift(top);
+    const float f = power_of_two(shift);
+    if (lane == 0) inv[row] = power_of_two(-shift);
+#pragma unroll
+    for (int i = 0; i < kStagePieces; ++i) {
+      const int64_t p = lane + i * kWave;
+      if (p < np) put(p, v[i], f);
+    }
   }
 }
 
@@ -405,8 +434,10 @@ hipError_t launch_stage(const void* x, int64_t rows, int64_t k, void* ws, const 
                                         up256(static_cast<size_t>(rows) * static_cast<size_t>(k) * 2));
   *xs = reinterpret_cast<const half_t*>(dst);
   *scale = inv;
-  void* argv[] = {&src, &dst, &inv, &k};
-  return launch_blocks(reinterpret_cast<const void*>(&stage_bf16_kernel), rows, 256, argv, 0, s);
+  void* argv[] = {&src, &dst, &inv, &rows, &k};
+  if (k > kStagePieces * kWave * 8)
+    return launch_blocks(reinterpret_cast<const void*>(&stage_bf16_kernel<true>), rows, 256, argv, 0, s);
+  return launch_blocks(reinterpret_cast<const void*>(&stage_bf16_kernel<false>), (rows + 3) / 4, 256, argv, 0, s);
 }
 
 size_t fused_gemm_bytes(int64_t m, int64_t n, int64_t k, DType xt, bool gated, bool grouped) {
