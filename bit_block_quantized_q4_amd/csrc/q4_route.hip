@@ -8,7 +8,9 @@
 // and one launch with their choice.
 //
 // Bound by latency and by the instructions of the choice: 4096 tokens of 256
-// experts are 2 MB of logits (0.4 us at 5 TB/s) and 0.6 MB of outputs.
+// experts are 2 MB of logits (0.4 us at 5 TB/s) and 0.6 MB of outputs; with groups,
+// a bias and eight chosen the choice takes 12.9 us and the plan 8.0.  16 tokens of
+// 128 experts: 8.0 us with the call.
 #include "q4_route_token.hpp"
 
 namespace q4 {
