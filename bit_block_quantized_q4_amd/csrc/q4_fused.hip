@@ -214,6 +214,7 @@ size_t product_workspace_bytes(int64_t m, int64_t topk, int64_t experts, int64_t
   size_t b = 0;
   const bool many = many_rows(m, topk, experts);
   if (xt == DType::BF16 && !fused_wave_supports(m, topk, experts, n, k, x_rows) &&
+      !(experts == 0 && fused_split_supports(m, gated ? n / 2 : n, n, k, true)) &&
       (many || fused_gemv_supports(n, k, x_rows, experts)))
     b += stage_bytes(x_rows, k);
   if (many) b += fused_gemm_bytes(m, n, k, xt, gated, experts != 0);
@@ -235,6 +236,9 @@ hipError_t launch_product(const Product& p, void* workspace, hipStream_t s) {
   const bool many = many_rows(p.m, p.topk, p.experts);
   if (p.xt != DType::F32 && fused_wave_supports(p.m, p.topk, p.experts, p.n, p.k, p.x_rows)) {
     e = launch_fused_wave(p, ep, plan_rows(p), plan_layout(p.m, p.topk, p.experts).max_tiles, s);
+  } else if (p.xt != DType::F32 && p.experts == 0 &&
+             fused_split_supports(p.m, ep.ldy, p.n, p.k, p.xt == DType::BF16)) {
+    e = launch_fused_split(p, ep, s);
   } else if (many || (p.xt != DType::F32 && fused_gemv_supports(p.n, p.k, p.x_rows, p.experts))) {
     const half_t* xs = static_cast<const half_t*>(p.x);
     const float* scale = nullptr;

@@ -199,6 +199,10 @@ bool fused_wave_supports(int64_t m, int64_t topk, int64_t experts, int64_t n, in
 hipError_t launch_fused_wave(const Product& p, const Epi& ep, const Rows& rows, int64_t max_tiles,
                              hipStream_t s);
 
+// Dense products of few rows and few row tiles (bf16 x, xb, as it is).
+bool fused_split_supports(int64_t m, int64_t nout, int64_t n, int64_t k, bool xb);
+hipError_t launch_fused_split(const Product& p, const Epi& ep, hipStream_t s);
+
 struct RouteArgs {
   const void* logits;
   DType dt;

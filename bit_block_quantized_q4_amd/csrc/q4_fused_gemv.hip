@@ -18,8 +18,7 @@
 //     a constant of the lane), and the last phase may be short; its copies and
 //     its waves' blocks stop at the row's end.
 // Ten rows of 5120 against 34816 gated weight rows: 23.7 us, 4.25 TB/s (a large
-// copy moves 4.8); one row against 7168 rows: 9.1 us, of which 4 are the start
-// and the join of two tiles per compute unit.
+// copy moves 4.8).  Narrow layers of few rows: see fused_split_kernel.
 #include "q4_fused.hpp"
 #include "q4_tile_geo.hpp"
 

@@ -1,5 +1,5 @@
-// Expert products for up to 16 rows per expert: every wavefront streams weight
-// rows by itself.
+// Products of up to 16 rows of which every wavefront streams weight rows by
+// itself: those of experts, and dense ones of few weight rows.
 //
 // An expert's matrix is small (a few MB) and a batch reaches many, so a
 // workgroup that fills, drains and reduces for every few rows of one spends
@@ -114,7 +114,90 @@ __global__ __launch_bounds__(kNW * kWave) void fused_wave_kernel(const half_t* _
   }
 }
 
+// Dense products whose row tiles are few (a decode layer's narrower linears): a
+// workgroup takes one row tile, its wavefronts a part of k each (whole chunks),
+// with the part's pieces of x, and their sums are added in the order of the
+// parts.  Nearly the whole matrix is then in flight at once, and no phase waits
+// for the slowest wavefront.  bf16: every wavefront scales its part of a row.
+constexpr int kSplitWaves = 8, kSplitRing = 3;
+
+struct SplitArgs {
+  Epi ep;
+  int m;
+};
+
+template <bool GATED, bool SHIFT, bool XB>
+__global__ __launch_bounds__(kSplitWaves * kWave) void fused_split_kernel(const half_t* __restrict__ x,
+                                                                          const uint8_t* __restrict__ W,
+                                                                          int64_t k, SplitArgs a) {
+  constexpr int kCols = GATED ? 8 : 16;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int waves = blockDim.x / kWave;
+  const int nch = static_cast<int>((k / kQK + kChunk - 1) / kChunk);
+  const int c0 = nch * wave / waves, c1 = nch * (wave + 1) / waves;
+  constexpr int kChunkPieces = kChunk * kQK / 8;  // of x
+  const int first = c0 * kChunkPieces;
+  const int np = (c1 < nch ? c1 * kChunkPieces : static_cast<int>(k / 8)) - first;
+  // LDS: every wavefront's rows and ring, then the sums [wave][row][16].
+  const int xstride = ((nch + waves - 1) / waves * kChunkPieces + 1) * 16;
+  const int own = a.m * xstride + kSplitRing * slot_bytes<SHIFT>;
+  uint8_t* const mine = smem + wave * own;
+  float* const sums = reinterpret_cast<float*>(smem + waves * own);
+  for (int row = 0; row < a.m; ++row)
+    for (int i0 = 0; i0 < np; i0 += kWave)
+      if (i0 + lane < np) dma16(x + row * k + 8 * (first + i0 + lane), mine + row * xstride + i0 * 16);
+  RowStream<kSplitRing, GATED, SHIFT> stream;
+  stream.begin(smem, wave * own + a.m * xstride, W, k, a.ep.ldy, a.ep.half, blockIdx.x, 1, 1);
+  stream.limit(c0, c1, 1);
+  wait_vm_upto<kCopies * kSplitRing>(stream.prologue());  // x, issued first, has landed
+  compiler_fence();
+  const int r = lane & 15, g = lane >> 4;
+  float sc[4] = {1.f, 1.f, 1.f, 1.f};
+  if constexpr (XB) {
+    for (int row = 0; row < a.m; ++row) {
+      const float f = stage_row_bf16(reinterpret_cast<u32x4*>(mine + row * xstride), np);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (row == 4 * g + e) sc[e] = f;
+    }
+    wait_lgkm0();
+    compiler_fence();
+  }
+  stream.run(mine + (r < a.m ? r : a.m - 1) * xstride + 8 * g, [&](int64_t, const float4_t& acc) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (4 * g + e < a.m) sums[(wave * a.m + 4 * g + e) * 16 + r] = acc[e] * sc[e];
+  });
+  __syncthreads();
+  for (int o = threadIdx.x; o < a.m * kCols; o += blockDim.x) {
+    const int row = o / kCols, c = o - row * kCols;
+    const int64_t col = blockIdx.x * int64_t{kCols} + c;
+    if (col >= a.ep.ldy) continue;
+    float z = 0.f, u = 0.f;
+    for (int w = 0; w < waves; ++w) {
+      const float* p = sums + (w * a.m + row) * 16 + (GATED ? 2 * c : c);
+      z += p[0];
+      if constexpr (GATED) u += p[1];
+    }
+    finish_store(a.ep, 0, row, col, z, u);
+  }
+}
+
 using KernelFn = const void*;
+
+// Wavefronts of a row tile: as many as there are chunks, up to eight.
+int split_waves(int64_t k) {
+  const int64_t nch = (k / kQK + kChunk - 1) / kChunk;
+  return static_cast<int>(nch < kSplitWaves ? nch : kSplitWaves);
+}
+int64_t split_lds(int64_t m, int64_t k, int waves) {
+  const int64_t nch = (k / kQK + kChunk - 1) / kChunk;
+  const int64_t xstride = ((nch + waves - 1) / waves * (kChunk * kQK / 8) + 1) * 16;
+  const int64_t slot = k % 256 != 0 ? slot_bytes<true> : slot_bytes<false>;
+  return waves * (m * xstride + kSplitRing * slot + m * 64);
+}
 
 // Rows staged at a time: no tile of distinct tokens has more.  (Fewer, with a
 // second pass for the fuller tiles, doubles the time of the whole launch.)
@@ -195,6 +278,43 @@ hipError_t launch_fused_wave(const Product& p, const Epi& ep, const Rows& rows, 
   }
   const int64_t n = grid(8, 1);
   return launch_form<8, 3>(x, xb, p.W, p.k, a, gated, shift, lds(8, 3), n, s);
+}
+
+// Up to eight rows (fp16) or four (bf16, whose rows every wavefront turns into
+// fp16 one after another), and row tiles for at most two workgroups per compute
+// unit at once.  Against the phase ring of q4_fused_gemv.hip (us, fp16 / bf16 with its
+// staging): 4096 x 4096, one row 5.8 and 6.9 / 6.1 and 9.3, four rows 6.1 and 6.8 /
+// 8.0 and 9.4; 7168 x 5120, one row 8.6 and 9.9 / 9.5 and 12.4.  Not taken:
+// 512 x 1024, 16 rows 5.3 and 4.7 / 12.5 and 7.0; 16384 x 2048 gated (four row tiles
+// per compute unit), one row 9.3 and 8.8.
+bool fused_split_supports(int64_t m, int64_t nout, int64_t n, int64_t k, bool xb) {
+  const int64_t tiles = (nout + (nout < n ? 7 : 15)) / (nout < n ? 8 : 16), cu = device_cu_count();
+  if (m > (xb ? 4 : 8) || k > (1 << 15) || tiles > 2 * cu || !fused_gemv_supports(n, k, m, 0)) return false;
+  return split_lds(m, k, split_waves(k)) <= (tiles <= cu ? kLdsMax : kLdsMax / 2);
+}
+
+hipError_t launch_fused_split(const Product& p, const Epi& ep, hipStream_t s) {
+  static const KernelFn fns[8] = {reinterpret_cast<KernelFn>(&fused_split_kernel<false, false, false>),
+                                  reinterpret_cast<KernelFn>(&fused_split_kernel<false, false, true>),
+                                  reinterpret_cast<KernelFn>(&fused_split_kernel<false, true, false>),
+                                  reinterpret_cast<KernelFn>(&fused_split_kernel<false, true, true>),
+                                  reinterpret_cast<KernelFn>(&fused_split_kernel<true, false, false>),
+                                  reinterpret_cast<KernelFn>(&fused_split_kernel<true, false, true>),
+                                  reinterpret_cast<KernelFn>(&fused_split_kernel<true, true, false>),
+                                  reinterpret_cast<KernelFn>(&fused_split_kernel<true, true, true>)};
+  static std::atomic<uint64_t> allowed[8];
+  const bool gated = ep.half != 0;
+  const int f = (gated ? 4 : 0) + (p.k % 256 != 0 ? 2 : 0) + (p.xt == DType::BF16 ? 1 : 0);
+  const hipError_t e = allow_dynamic_lds(fns[f], kLdsMax, allowed[f]);
+  if (e != hipSuccess) return e;
+  const int waves = split_waves(p.k);
+  const half_t* x = static_cast<const half_t*>(p.x);
+  const uint8_t* W = p.W;
+  int64_t k = p.k;
+  SplitArgs a{ep, static_cast<int>(p.m)};
+  void* argv[] = {&x, &W, &k, &a};
+  return launch_blocks(fns[f], (ep.ldy + (gated ? 7 : 15)) / (gated ? 8 : 16), waves * kWave, argv,
+                       static_cast<size_t>(split_lds(p.m, p.k, waves)), s);
 }
 
 }  // namespace q4

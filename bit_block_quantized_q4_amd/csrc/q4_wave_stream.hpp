@@ -111,6 +111,13 @@ struct RowStream {
     cl = issued = 0;
     if (total > 0) set_tile();
   }
+  // Of every row only the chunks c0 .. c1 - 1 (before the prologue).
+  __device__ __forceinline__ void limit(int c0, int c1, int ntiles) {
+    wbase += c0 * kSeg;
+    if (c1 < nch) last = kChunk;
+    nch = c1 - c0;
+    total = ntiles * nch;
+  }
   // Weight row of slot row r of row tile t (columns past the last repeat it).
   __device__ __forceinline__ int64_t wrow(int64_t t, int r) const {
     int64_t c = t * kCols + (GATED ? r >> 1 : r);

@@ -224,10 +224,10 @@ size_t q4_linear_workspace_size(int64_t m, int64_t n, int64_t k, int x_dtype, in
  *     exact integers and the block scales in fp32, as in q4_gemv; above, the
  *     weights are dequantised to fp16 (one rounding, 2^-11 relative) as in
  *     q4_gemm, with the exact route for tiles where that overflows.
- *   - bf16 x may be staged as fp16, every row multiplied by the power of two
- *     that brings its largest magnitude to [2^15, 2^16): exact for every
- *     value of at least 2^-32 of that magnitude; a smaller one is rounded to
- *     a multiple of 2^-39 of it.
+ *   - bf16 x may be staged as fp16, every row or part of a row multiplied by
+ *     the power of two that brings its largest magnitude to [2^15, 2^16):
+ *     exact for every value of at least 2^-32 of that magnitude; a smaller one
+ *     is rounded to a multiple of 2^-39 of it.
  * `workspace` holds q4_linear_workspace_size bytes (NULL when that is 0),
  * overlaps no other buffer and is shared by no call that may run at the same
  * time (calls on several streams, graphs replayed at once). */

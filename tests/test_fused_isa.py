@@ -9,7 +9,7 @@ from test_isa import HIPCC, asm, pytestmark  # noqa: F401
 
 
 @pytest.mark.parametrize("src,pattern", [("q4_fused_gemv.hip", "fused_gemv_kernel"),
-                                         ("q4_fused_wave.hip", "fused_wave_kernel"),
+                                         ("q4_fused_wave.hip", "fused_"),
                                          ("q4_moe_one.hip", "moe_one_")])
 def test_dynamic_lds_kernels_have_no_static_lds(src, pattern):
     """They may ask for all 160 KB of a compute unit."""

@@ -155,3 +155,14 @@ def test_both_ways_from_python_agree_and_refuse_alike(q4lib, gpu):
         q4lib.q4_route(dev(rows(5, "f32", 3, 8), gpu), 9)
     with pytest.raises(q4lib.Q4Error):
         q4lib.q4_route(dev(rows(5, "f32", 3, 9), gpu), 2, groups=2)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 4112, 2112), (2, 8192, 320), (8, 514, 2048), (4, 4096, 4160), (3, 8180, 704),
+                                   (1, 16, 16384), (7, 100, 8192), (5, 2050, 1088), (1, 8194, 576), (6, 34, 2304)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+def test_linear_rows_split_over_wavefronts(q4lib, gpu, m, n, k, gated, xt):
+    """Narrow layers: parts of k of unequal length, a short last chunk, fewer chunks
+    than wavefronts, one and two row tiles per compute unit and just more."""
+    run_linear(q4lib, gpu, m, n, k, xt, act="silu", gated=gated, bias=xt, residual=True, seed=m + k)
+    run_linear(q4lib, gpu, m, n, k, xt, "f32", gated=gated, inplace=True, residual=True, seed=m)
