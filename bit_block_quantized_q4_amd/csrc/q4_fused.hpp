@@ -118,6 +118,18 @@ __device__ __forceinline__ uint32_t bf16x2_scaled_to_f16x2(uint32_t v, float f) 
   return __builtin_bit_cast(uint32_t, h);
 }
 
+// dma16_sbase (NT: the non-temporal one) behind five wait states.  A vector
+// instruction's write of a scalar register, such as the read back of a spilled one,
+// must be that far from its use as an address; the compiler does not see to it
+// before inline assembly (a build without them faulted).
+template <bool NT>
+__device__ __forceinline__ void copy16(uint32_t voff, const void* sbase, uint32_t lds) {
+  if constexpr (NT)
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+  else
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+}
+
 // silu and the tanh form of gelu as z / (1 + exp(-t)): no cancellation for
 // negative z, and 0 (not NaN) where exp overflows.
 __device__ __forceinline__ float activate(float z, int act) {

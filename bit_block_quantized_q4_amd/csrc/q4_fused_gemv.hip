@@ -147,16 +147,14 @@ __global__ __launch_bounds__((NW + NP) * kWave, 1) void fused_gemv_kernel(const 
         constexpr int q = decltype(cc)::value;
         if ((wa >> q) & 1u) {
           if ((wl >> q) & 1u) {
-            const uint32_t dst = sb + (q * CW + cwave) * (kWave * 16);
-            if constexpr (T <= 2) dma16_sbase_nt(wsrc[q], ws, dst);
-            else dma16_sbase(wsrc[q], ws, dst);
+            copy16<T <= 2>(wsrc[q], ws, sb + (q * CW + cwave) * (kWave * 16));
           }
         }
       });
       unroll<0, G::nix_max>([&](auto cc) {
         constexpr int q = decltype(cc)::value;
         if ((xa >> q) & 1u) {
-          if ((xl >> q) & 1u) dma16_sbase(xsrc[q], xs, sb + G::wbytes + (q * CW + cwave) * (kWave * 16));
+          if ((xl >> q) & 1u) copy16<false>(xsrc[q], xs, sb + G::wbytes + (q * CW + cwave) * (kWave * 16));
         }
       });
     };

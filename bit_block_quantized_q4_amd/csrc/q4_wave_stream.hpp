@@ -139,7 +139,7 @@ struct RowStream {
     const int slot = issued % kRing;
 #pragma unroll
     for (int q = 0; q < kCopies; ++q)
-      if (need[q] < bytes) dma16_sbase(src[q], base, ring + slot * slot_bytes<SHIFT> + q * (kWave * 16));
+      if (need[q] < bytes) copy16<false>(src[q], base, ring + slot * slot_bytes<SHIFT> + q * (kWave * 16));
     ++issued;
     if (++cl == nch) {
       cl = 0;
