@@ -166,3 +166,12 @@ def test_linear_rows_split_over_wavefronts(q4lib, gpu, m, n, k, gated, xt):
     than wavefronts, one and two row tiles per compute unit and just more."""
     run_linear(q4lib, gpu, m, n, k, xt, act="silu", gated=gated, bias=xt, residual=True, seed=m + k)
     run_linear(q4lib, gpu, m, n, k, xt, "f32", gated=gated, inplace=True, residual=True, seed=m)
+
+
+@pytest.mark.parametrize("m", [1, 4, 10, 32])
+@pytest.mark.parametrize("yt", ["f16", "f32"])
+def test_plain_products_are_the_decode_gemv(q4lib, gpu, m, yt):
+    packed, _ = weights(m, 130, 608)
+    x, pd = rows(m + 1, "f16", m, 608).to(gpu), packed.to(gpu)
+    want = q4lib.q4_gemv(x, pd, y_dtype=TYPES[yt])
+    assert torch.equal(q4lib.q4_linear(x, pd, y_dtype=TYPES[yt]), want)
