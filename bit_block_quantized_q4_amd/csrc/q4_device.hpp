@@ -54,16 +54,23 @@ typedef __attribute__((address_space(3))) void* lptr_t;
 // lds + 16 * l (the LDS base, held in M0, must be uniform across the wave).
 // Issued as inline asm so that the compiler tracks no LDS-DMA writes of its
 // own: every wait on these copies is the explicit wait_vm below.
+// Hardware does not wait for M0 or, in the scalar-base form, for an address
+// that a vector instruction wrote (the read back of a spilled one): a copy must
+// be one wait state behind a scalar write of M0, five behind a vector write of
+// M0 or of its address, and the compiler sees to neither before inline assembly.
+// The s_nop gives M0's; in the scalar-base form a scalar move of the address
+// does, and is itself waited for.  That nothing but scalar instructions writes
+// M0 is checked on the assembly (tests/test_copy_wait_states.py).
 __device__ __forceinline__ void dma16(const void* src, void* lds) {
   const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lptr_t)(lds)));
-  asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(base) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(base) : "memory");
 }
 // As dma16 with the non-temporal hint (nt): for bytes read once per launch,
 // the packed weights of the decode GEMV, which are then not kept in the
 // caches in place of data that is read again (the activations).
 __device__ __forceinline__ void dma16_nt(const void* src, void* lds) {
   const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lptr_t)(lds)));
-  asm volatile("global_load_lds_dwordx4 %0, off nt" ::"v"(src), "{m0}"(base) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(src), "{m0}"(base) : "memory");
 }
 
 // Wait until at most N vector-memory operations of this wave are in flight.
@@ -156,11 +163,15 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // pair) plus a 32-bit per-lane byte offset; lane l's 16 bytes land at LDS byte
 // address lds + 16 * l (lds uniform, held in M0).  Untracked like dma16.
 __device__ __forceinline__ void dma16_sbase(uint32_t voff, const void* sbase, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+  uint64_t base;
+  asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
+               : "=s"(base) : "v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
 }
 // As dma16_sbase with the non-temporal hint (see dma16_nt).
 __device__ __forceinline__ void dma16_sbase_nt(uint32_t voff, const void* sbase, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+  uint64_t base;
+  asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0 nt"
+               : "=s"(base) : "v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lptr_t)(p)));

@@ -118,10 +118,9 @@ __device__ __forceinline__ uint32_t bf16x2_scaled_to_f16x2(uint32_t v, float f) 
   return __builtin_bit_cast(uint32_t, h);
 }
 
-// dma16_sbase (NT: the non-temporal one) behind five wait states.  A vector
-// instruction's write of a scalar register, such as the read back of a spilled one,
-// must be that far from its use as an address; the compiler does not see to it
-// before inline assembly (a build without them faulted).
+// dma16_sbase (NT: the non-temporal one) with five wait states in place of the
+// scalar move (see dma16): the form for kernels whose scalar registers spill.  (A
+// build without either read a spilled address too early, and faulted.)
 template <bool NT>
 __device__ __forceinline__ void copy16(uint32_t voff, const void* sbase, uint32_t lds) {
   if constexpr (NT)
