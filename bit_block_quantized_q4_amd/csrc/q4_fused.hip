@@ -202,6 +202,26 @@ hipError_t launch_row(const Product& p, const Epi& ep0, hipStream_t s) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+// Whether the decode GEMV takes a plain product of few fp16 rows in less time than
+// the kernels here, whose addresses and masks for gates, gathered rows and any k
+// take longer to set up (device us, GEMV / here, rows of x in front):
+//   k % 512 == 0, its matrix-core kernels: always (5120 x 5120: 1 row 6.1 / 8.3,
+//     10 rows 7.1 / 9.6, 32 rows 9.8 / 11.8);
+//   k % 256 == 0, its streaming kernel: up to 16 rows and one row tile per compute
+//     unit (4096 x 11008: 1 row 9.2 / 10.0, 16 rows 12.7 / 14.5; but 17 rows 18.2 /
+//     16.9, 12288 x 3328: 1 row 11.4 / 9.4, 8192 x 1280: 16 rows 7.5 / 5.9);
+//   other k % 64 == 0, its general kernel: one or two rows of a small layer (2048 x
+//     1408: 1 row 3.2 / 4.4, 2 rows 3.5 / 4.4; 2048 x 8640: 1 row 6.9 / 8.6; but
+//     10 rows of 2048 x 1408 9.2 / 4.8, 4096 x 4160: 1 row 7.3 / 6.3);
+//   what only the row kernel here takes: always (5120 x 1056: 1 row 3.8 / 6.9, 32
+//     rows 39 / 44).
+bool gemv_is_faster(int64_t m, int64_t n, int64_t k) {
+  if (k % 512 == 0 || !fused_gemv_supports(n, k, m, 0)) return true;
+  const int64_t cu = device_cu_count();
+  if (k % 256 == 0) return m <= 16 && n <= 16 * cu;
+  return m <= 2 && m * n <= (k <= 2048 ? 20 : 8) * cu;
+}
+
 }  // namespace
 
 // Rows of a product from which it runs on the prefill tiles.
@@ -234,12 +254,9 @@ hipError_t launch_product(const Product& p, void* workspace, hipStream_t s) {
   }
   hipError_t e = hipSuccess;
   const bool many = many_rows(p.m, p.topk, p.experts);
-  // A plain product of few fp16 rows is the decode GEMV's (7168 x 5120, m = 10: 8.0
-  // us against 10.3 here, where addresses and masks for gates, gathered rows and
-  // any k take longer to set up; m = 1: 7.2 against 8.6).
   const bool plain = p.experts == 0 && ep.half == 0 && ep.act == kActNone && ep.bias == nullptr &&
                      ep.residual == nullptr && ep.y_dt != static_cast<int>(DType::BF16);
-  if (plain && !many && p.xt == DType::F16) {
+  if (plain && !many && p.xt == DType::F16 && gemv_is_faster(p.m, p.n, p.k)) {
     e = launch_gemv(p.x, p.xt, p.W, ep.y, static_cast<DType>(ep.y_dt), static_cast<int>(p.m), p.n, p.k, s);
   } else if (p.xt != DType::F32 && fused_wave_supports(p.m, p.topk, p.experts, p.n, p.k, p.x_rows)) {
     e = launch_fused_wave(p, ep, plan_rows(p), plan_layout(p.m, p.topk, p.experts).max_tiles, s);
