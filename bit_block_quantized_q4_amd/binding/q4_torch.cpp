@@ -5,7 +5,7 @@
 // the call is an ordinary one (contiguous device tensors of the current device
 // with the right shapes and types), allocates what it returns, and calls the
 // C entry point, whose address it was given.  It returns None for any other
-// call and for any status but OK, before which nothing has been launched: the
+// call and for any status but OK (a refused call has launched nothing): the
 // Python function then takes its own full way, with its own errors.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

@@ -80,8 +80,24 @@ q4_status check_matmul(const void* x, int x_dtype, const void* packed, void* y,
 
 // ------------------------------------------------------------------ fused
 
-// A grid that no launch holds (launch_blocks) is a matter of the shape.
-q4_status from_launch(hipError_t e) { return e == hipErrorInvalidConfiguration ? Q4_ERR_SHAPE : from_hip(e); }
+// A product without its buffers.  experts == 0: dense.
+q4::Product make_product(int x_dtype, int64_t x_rows, int64_t m, int64_t n, int64_t k, int64_t topk = 1,
+                         int64_t experts = 0, bool combine = false) {
+  q4::Product p;
+  p.xt = static_cast<q4::DType>(x_dtype);
+  p.x_rows = x_rows;
+  p.m = m;
+  p.n = n;
+  p.k = k;
+  p.topk = topk;
+  p.experts = experts;
+  p.combine = combine;
+  return p;
+}
+
+// Whether a grid holds every launch of a product: a matter of the shape, settled
+// before the first of them.
+bool fits(const q4::Product& p) { return q4::launch_product(p, nullptr, q4::Queue{nullptr, true}) == hipSuccess; }
 
 constexpr int64_t kMaxPairs = int64_t(1) << 24;  // tokens x experts each
 
@@ -129,6 +145,16 @@ q4_status check_product(const void* x, int x_dtype, int64_t x_rows, const void* 
       return Q4_ERR_INVALID_ARG;
   }
   return Q4_OK;
+}
+
+// For the sizes: some epilogue, so that the product is none that q4_gemv takes
+// (which needs no workspace).
+q4::Epi size_epi(int64_t n, bool gate) {
+  q4::Epi e;
+  e.act = q4::kActRelu;
+  e.ldy = gate ? n / 2 : n;
+  e.half = gate ? n / 2 : 0;
+  return e;
 }
 
 q4::Epi make_epi(const q4_epilogue* ep, void* y, int y_dtype, int64_t n) {
@@ -296,7 +322,10 @@ size_t q4_linear_workspace_size(int64_t m, int64_t n, int64_t k, int x_dtype, in
   if (!valid_linear(m, n, k) || !valid_in_dtype(x_dtype) || gate < 0 || gate > 1 ||
       (gate && n % 2 != 0))
     return 0;
-  return q4::product_workspace_bytes(m, 1, 0, n, k, m, static_cast<q4::DType>(x_dtype), gate == 1, false);
+  q4::Product p = make_product(x_dtype, m, m, n, k);
+  p.ep = size_epi(n, gate == 1);
+  if (!fits(p)) return 0;
+  return q4::product_workspace_bytes(m, 1, 0, n, k, m, p.xt, gate == 1, false);
 }
 
 q4_status q4_linear(const void* x, int x_dtype, const void* packed, const q4_epilogue* epilogue,
@@ -308,15 +337,12 @@ q4_status q4_linear(const void* x, int x_dtype, const void* packed, const q4_epi
   const q4_status st = check_product(x, x_dtype, m, packed, 1, epilogue, y, y_dtype, m, n, k, workspace,
                                      need, workspace_bytes, {nullptr, 0}, {nullptr, 0});
   if (st != Q4_OK) return st;
-  q4::Product p;
+  q4::Product p = make_product(x_dtype, m, m, n, k);
   p.x = x;
-  p.xt = static_cast<q4::DType>(x_dtype);
-  p.x_rows = p.m = m;
   p.W = static_cast<const uint8_t*>(packed);
-  p.n = n;
-  p.k = k;
   p.ep = make_epi(epilogue, y, y_dtype, n);
-  return from_launch(q4::launch_product(p, workspace, reinterpret_cast<hipStream_t>(stream)));
+  if (!fits(p)) return Q4_ERR_SHAPE;
+  return from_hip(q4::launch_product(p, workspace, q4::Queue{reinterpret_cast<hipStream_t>(stream)}));
 }
 
 size_t q4_route_plan_size(int64_t m, int64_t topk, int64_t experts) {
@@ -358,8 +384,10 @@ size_t q4_experts_workspace_size(int64_t m, int64_t topk, int64_t experts, int64
   if (!valid_experts(m, topk, experts, n, k) || (x_rows != m && x_rows != m * topk) ||
       !valid_in_dtype(x_dtype) || gate < 0 || gate > 1 || (gate && n % 2 != 0))
     return 0;
-  return q4::product_workspace_bytes(m, topk, experts, n, k, x_rows, static_cast<q4::DType>(x_dtype),
-                                     gate == 1, combine != 0);
+  q4::Product p = make_product(x_dtype, x_rows, m, n, k, topk, experts, combine != 0);
+  p.ep = size_epi(n, gate == 1);
+  if (!fits(p)) return 0;
+  return q4::product_workspace_bytes(m, topk, experts, n, k, x_rows, p.xt, gate == 1, combine != 0);
 }
 
 q4_status q4_experts(const void* x, int x_dtype, int64_t x_rows, const void* packed,
@@ -376,20 +404,14 @@ q4_status q4_experts(const void* x, int x_dtype, int64_t x_rows, const void* pac
       need, workspace_bytes, {plan, q4_route_plan_size(m, topk, experts)},
       {weights, weights ? static_cast<size_t>(m * topk) * 4 : 0});
   if (st != Q4_OK) return st;
-  q4::Product p;
+  q4::Product p = make_product(x_dtype, x_rows, m, n, k, topk, experts, weights != nullptr);
   p.x = x;
-  p.xt = static_cast<q4::DType>(x_dtype);
-  p.x_rows = x_rows;
-  p.m = m;
   p.W = static_cast<const uint8_t*>(packed);
-  p.n = n;
-  p.k = k;
-  p.topk = topk;
-  p.experts = experts;
   p.plan = static_cast<const int*>(plan);
   p.weights = weights;
   p.ep = make_epi(epilogue, y, y_dtype, n);
-  return from_launch(q4::launch_product(p, workspace, reinterpret_cast<hipStream_t>(stream)));
+  if (!fits(p)) return Q4_ERR_SHAPE;
+  return from_hip(q4::launch_product(p, workspace, q4::Queue{reinterpret_cast<hipStream_t>(stream)}));
 }
 
 }  // extern "C"
@@ -423,6 +445,32 @@ bool valid_moe(int64_t m, int64_t topk, int64_t experts, int64_t hidden, int64_t
          valid_experts(m, topk, experts, hidden, inter);
 }
 
+// The two products of a layer, without their buffers.
+struct MoeProducts {
+  q4::Product up, down;
+};
+
+MoeProducts moe_products(int64_t m, int64_t topk, int64_t experts, int64_t hidden, int64_t inter, int x_dtype,
+                         bool gate) {
+  const int64_t nup = gate ? 2 * inter : inter;
+  MoeProducts p{make_product(x_dtype, m, m, nup, hidden, topk, experts),
+                make_product(x_dtype, m * topk, m, hidden, inter, topk, experts, true)};
+  p.up.ep = size_epi(nup, gate);
+  p.down.ep = size_epi(hidden, false);
+  return p;
+}
+
+// As fits, for the launches of a layer.  (The routing's always do.)
+bool moe_fits(const MoeProducts& p) {
+  q4::RouteArgs r{};
+  r.m = p.up.m;
+  r.topk = p.up.topk;
+  r.experts = p.up.experts;
+  if (q4::moe_one_supports(r, p.up, p.down))
+    return q4::launch_moe_one(r, p.up, p.down, q4::Queue{nullptr, true}) == hipSuccess;
+  return fits(p.up) && fits(p.down);
+}
+
 }  // namespace
 
 extern "C" {
@@ -430,7 +478,8 @@ extern "C" {
 size_t q4_moe_workspace_size(int64_t m, int64_t topk, int64_t experts, int64_t hidden, int64_t inter,
                              int x_dtype, int gate) {
   if (gate < 0 || gate > 1 || !valid_in_dtype(x_dtype) || topk > experts ||
-      !valid_moe(m, topk, experts, hidden, inter, gate == 1))
+      !valid_moe(m, topk, experts, hidden, inter, gate == 1) ||
+      !moe_fits(moe_products(m, topk, experts, hidden, inter, x_dtype, gate == 1)))
     return 0;
   return moe_layout(m, topk, experts, hidden, inter, x_dtype, gate == 1).total;
 }
@@ -450,6 +499,8 @@ q4_status q4_moe(const void* x, int x_dtype, const void* logits, int logits_dtyp
   if (!valid_moe(m, topk, experts, hidden, inter, gate)) return Q4_ERR_SHAPE;
   if (!valid_in_dtype(x_dtype)) return Q4_ERR_DTYPE;
   if (!aligned16(ids) || !aligned16(weights)) return Q4_ERR_ALIGNMENT;
+  MoeProducts products = moe_products(m, topk, experts, hidden, inter, x_dtype, gate);
+  if (!moe_fits(products)) return Q4_ERR_SHAPE;
   const MoeLayout L = moe_layout(m, topk, experts, hidden, inter, x_dtype, gate);
   if (!workspace || workspace_bytes < L.total) return Q4_ERR_WORKSPACE;
   if (!aligned16(workspace)) return Q4_ERR_ALIGNMENT;
@@ -489,30 +540,21 @@ q4_status q4_moe(const void* x, int x_dtype, const void* logits, int logits_dtyp
   if (overlaps_any(ys, {xs, us})) return Q4_ERR_INVALID_ARG;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const q4::RouteArgs ra = make_route(logits, logits_dtype, m, experts, topk, *routing, wids, ww, base);
-  q4::Product p;
+  q4::Product &p = products.up, &d = products.down;
   p.x = x;
-  p.xt = static_cast<q4::DType>(x_dtype);
-  p.x_rows = p.m = m;
   p.W = static_cast<const uint8_t*>(up);
-  p.n = nup;
-  p.k = hidden;
-  p.topk = topk;
-  p.experts = experts;
-  p.plan = reinterpret_cast<const int*>(base);
+  p.plan = d.plan = reinterpret_cast<const int*>(base);
   p.ep = make_epi(up_epilogue, h, x_dtype, nup);
-  q4::Product d = p;
   d.x = h;
-  d.x_rows = m * topk;
   d.W = static_cast<const uint8_t*>(down);
-  d.n = hidden;
-  d.k = inter;
   d.weights = ww;
   d.ep = make_epi(down_epilogue, y, y_dtype, hidden);
-  if (q4::moe_one_supports(ra, p, d)) return from_launch(q4::launch_moe_one(ra, p, d, st));
+  const q4::Queue q{st};
+  if (q4::moe_one_supports(ra, p, d)) return from_hip(q4::launch_moe_one(ra, p, d, q));
   hipError_t e = q4::launch_route(ra, st);
-  if (e == hipSuccess) e = q4::launch_product(p, pw, st);
-  if (e == hipSuccess) e = q4::launch_product(d, pw, st);
-  return from_launch(e);
+  if (e == hipSuccess) e = q4::launch_product(p, pw, q);
+  if (e == hipSuccess) e = q4::launch_product(d, pw, q);
+  return from_hip(e);
 }
 
 }  // extern "C"

@@ -177,8 +177,10 @@ Rows plan_rows(const Product& p) {
   Rows r;
   if (p.experts == 0) return r;
   const PlanLayout L = plan_layout(p.m, p.topk, p.experts);
-  r.recs = p.plan + L.tiles;
-  r.ntiles = p.plan + L.head;
+  if (p.plan != nullptr) {
+    r.recs = p.plan + L.tiles;
+    r.ntiles = p.plan + L.head;
+  }
   r.rec_words = L.rec_words;
   r.xdiv = p.x_rows == p.m ? static_cast<int>(p.topk) : 1;
   r.wstride = p.n * (p.k / kQK) * kBlockBytes;
@@ -187,7 +189,7 @@ Rows plan_rows(const Product& p) {
 }
 
 template <typename XT>
-hipError_t launch_row(const Product& p, const Epi& ep0, hipStream_t s) {
+hipError_t launch_row(const Product& p, const Epi& ep0, Queue q) {
   Epi ep = ep0;
   Rows rows = plan_rows(p);
   const XT* x = static_cast<const XT*>(p.x);
@@ -197,7 +199,7 @@ hipError_t launch_row(const Product& p, const Epi& ep0, hipStream_t s) {
   void* argv[] = {&x, &W, &m, &nout, &k, &cblocks, &ep, &rows};
   const void* fn = ep.half != 0 ? reinterpret_cast<const void*>(&fused_row_kernel<XT, 2>)
                                 : reinterpret_cast<const void*>(&fused_row_kernel<XT, 1>);
-  return launch_blocks(fn, cblocks * tiles, 256, argv, 0, s);
+  return launch_blocks(fn, cblocks * tiles, 256, argv, 0, q);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -242,50 +244,51 @@ size_t product_workspace_bytes(int64_t m, int64_t topk, int64_t experts, int64_t
   return b;
 }
 
-hipError_t launch_product(const Product& p, void* workspace, hipStream_t s) {
+hipError_t launch_product(const Product& p, void* workspace, Queue q) {
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Epi ep = p.ep;
   const float* part = reinterpret_cast<const float*>(ws);
-  if (p.weights != nullptr) {  // fp32 rows first, then their sums
+  if (p.combine) {  // fp32 rows first, then their sums
     ep.y = ws;
     ep.y_dt = static_cast<int>(DType::F32);
     ep.residual = nullptr;
-    ws += up256(static_cast<size_t>(p.m * p.topk) * static_cast<size_t>(ep.ldy) * 4);
+    ws = behind(ws, up256(static_cast<size_t>(p.m * p.topk) * static_cast<size_t>(ep.ldy) * 4));
   }
   hipError_t e = hipSuccess;
   const bool many = many_rows(p.m, p.topk, p.experts);
   const bool plain = p.experts == 0 && ep.half == 0 && ep.act == kActNone && ep.bias == nullptr &&
                      ep.residual == nullptr && ep.y_dt != static_cast<int>(DType::BF16);
   if (plain && !many && p.xt == DType::F16 && gemv_is_faster(p.m, p.n, p.k)) {
-    e = launch_gemv(p.x, p.xt, p.W, ep.y, static_cast<DType>(ep.y_dt), static_cast<int>(p.m), p.n, p.k, s);
+    if (!q.dry)  // (one launch)
+      e = launch_gemv(p.x, p.xt, p.W, ep.y, static_cast<DType>(ep.y_dt), static_cast<int>(p.m), p.n, p.k, q.s);
   } else if (p.xt != DType::F32 && fused_wave_supports(p.m, p.topk, p.experts, p.n, p.k, p.x_rows)) {
-    e = launch_fused_wave(p, ep, plan_rows(p), plan_layout(p.m, p.topk, p.experts).max_tiles, s);
+    e = launch_fused_wave(p, ep, plan_rows(p), plan_layout(p.m, p.topk, p.experts).max_tiles, q);
   } else if (p.xt != DType::F32 && p.experts == 0 &&
              fused_split_supports(p.m, ep.ldy, p.n, p.k, p.xt == DType::BF16)) {
-    e = launch_fused_split(p, ep, s);
+    e = launch_fused_split(p, ep, q);
   } else if (many || (p.xt != DType::F32 && fused_gemv_supports(p.n, p.k, p.x_rows, p.experts))) {
     const half_t* xs = static_cast<const half_t*>(p.x);
     const float* scale = nullptr;
     if (p.xt == DType::BF16) {
-      e = launch_stage(p.x, p.x_rows, p.k, ws, &xs, &scale, s);
+      e = launch_stage(p.x, p.x_rows, p.k, ws, &xs, &scale, q);
       if (e != hipSuccess) return e;
-      ws += stage_bytes(p.x_rows, p.k);
+      ws = behind(ws, stage_bytes(p.x_rows, p.k));
     }
     PlanLayout L{};
     if (p.experts != 0) L = plan_layout(p.m, p.topk, p.experts);
-    if (many) e = launch_fused_gemm(p, ep, plan_rows(p), xs, scale, L.max_tiles, ws, s);
-    else e = launch_fused_gemv(p, ep, plan_rows(p), xs, scale, L.max_tiles, L.tile_rows, s);
+    if (many) e = launch_fused_gemm(p, ep, plan_rows(p), xs, scale, L.max_tiles, ws, q);
+    else e = launch_fused_gemv(p, ep, plan_rows(p), xs, scale, L.max_tiles, L.tile_rows, q);
   } else if (p.xt == DType::F32) {
-    e = launch_row<float>(p, ep, s);
+    e = launch_row<float>(p, ep, q);
   } else if (p.xt == DType::F16) {
-    e = launch_row<half_t>(p, ep, s);
+    e = launch_row<half_t>(p, ep, q);
   } else {
-    e = launch_row<bf16_t>(p, ep, s);
+    e = launch_row<bf16_t>(p, ep, q);
   }
-  if (e != hipSuccess || p.weights == nullptr) return e;
+  if (e != hipSuccess || !p.combine) return e;
   const PlanLayout L = plan_layout(p.m, p.topk, p.experts);
   const float* w = p.weights;
-  const int* pos = p.plan + L.pos;
+  const int* pos = p.plan != nullptr ? p.plan + L.pos : nullptr;
   int64_t nout = ep.ldy;
   const int v = nout % 4 == 0 ? 4 : 1;
   int topk = static_cast<int>(p.topk), cblocks = static_cast<int>((nout + 256 * v - 1) / (256 * v));
@@ -293,7 +296,7 @@ hipError_t launch_product(const Product& p, void* workspace, hipStream_t s) {
   void* argv[] = {&part, &w, &pos, &topk, &nout, &cblocks, &out};
   const void* fn = v == 4 ? reinterpret_cast<const void*>(&combine_kernel<4>)
                           : reinterpret_cast<const void*>(&combine_kernel<1>);
-  return launch_blocks(fn, p.m * cblocks, 256, argv, 0, s);
+  return launch_blocks(fn, p.m * cblocks, 256, argv, 0, q);
 }
 
 }  // namespace q4

@@ -163,56 +163,74 @@ __device__ __forceinline__ void finish_store(const Epi& ep, int64_t boff, int64_
 
 // ------------------------------------------------------------------ launchers
 
+// Where launches go.  A dry run of a call makes none, reads no pointer and asks no
+// device for anything but its compute units: it says whether a grid holds every one
+// of the call's launches, before the first.
+struct Queue {
+  hipStream_t s = nullptr;
+  bool dry = false;
+};
+
 // A launch of x * y * z workgroups.  One that a grid does not hold (2^32 threads
 // along x, 65535 workgroups along y or z) is refused here instead of cut short.
-inline hipError_t launch_blocks(const void* fn, int64_t x, int threads, void** argv, size_t lds, hipStream_t s,
-                                int64_t y = 1, int64_t z = 1) {
+// dynamic: bytes of dynamic LDS that the kernel has to be allowed, noted in `allowed`.
+inline hipError_t launch_blocks(const void* fn, int64_t x, int threads, void** argv, size_t lds, Queue q,
+                                int64_t y = 1, int64_t z = 1, int dynamic = 0,
+                                std::atomic<uint64_t>* allowed = nullptr) {
   if (x < 1 || x > ((int64_t{1} << 32) - 1) / threads || y < 1 || y > 65535 || z < 1 || z > 65535)
     return hipErrorInvalidConfiguration;
+  if (q.dry) return hipSuccess;
+  if (allowed != nullptr) {
+    const hipError_t e = allow_dynamic_lds(fn, dynamic, *allowed);
+    if (e != hipSuccess) return e;
+  }
   return hipLaunchKernel(fn, dim3(static_cast<unsigned>(x), static_cast<unsigned>(y), static_cast<unsigned>(z)),
-                         dim3(static_cast<unsigned>(threads)), argv, lds, s);
+                         dim3(static_cast<unsigned>(threads)), argv, lds, q.s);
 }
+
+// p + n bytes; of a null pointer (dry runs have no buffers) itself.
+inline uint8_t* behind(void* p, size_t n) { return p != nullptr ? static_cast<uint8_t*>(p) + n : nullptr; }
 
 // A product as the launchers take it.
 struct Product {
-  const void* x;
+  const void* x = nullptr;
   DType xt;
   int64_t x_rows;
-  const uint8_t* W;
+  const uint8_t* W = nullptr;
   int64_t m;  // rows of one group (dense), or tokens
   int64_t n, k;
   int64_t topk = 1, experts = 0;  // experts == 0: dense
   const int* plan = nullptr;      // experts: the plan's words
-  const float* weights = nullptr; // experts, combined
+  bool combine = false;           // experts: rows summed by `weights`
+  const float* weights = nullptr;
   Epi ep;
 };
 
 size_t product_workspace_bytes(int64_t m, int64_t topk, int64_t experts, int64_t n, int64_t k,
                                int64_t x_rows, DType xt, bool gated, bool combine);
-hipError_t launch_product(const Product& p, void* workspace, hipStream_t s);
+hipError_t launch_product(const Product& p, void* workspace, Queue q);
 
 // Matrix-core products of many rows (16-bit x, and fp32 x on the exact route).
 size_t stage_bytes(int64_t rows, int64_t k);
 hipError_t launch_stage(const void* x, int64_t rows, int64_t k, void* ws, const half_t** xs,
-                        const float** scale, hipStream_t s);
+                        const float** scale, Queue q);
 size_t fused_gemm_bytes(int64_t m, int64_t n, int64_t k, DType xt, bool gated, bool grouped);
 hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
-                             const float* xscale, int64_t row_tiles, void* workspace, hipStream_t s);
+                             const float* xscale, int64_t row_tiles, void* workspace, Queue q);
 
 // Matrix-core products of few rows (16-bit x as fp16).
 bool fused_gemv_supports(int64_t n, int64_t k, int64_t x_rows, int64_t experts);
 hipError_t launch_fused_gemv(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
-                             const float* xscale, int64_t max_tiles, int tile_rows, hipStream_t s);
+                             const float* xscale, int64_t max_tiles, int tile_rows, Queue q);
 
 // Expert products of at most 16 rows per tile, streamed by single wavefronts.
 // They take bf16 x as it is.
 bool fused_wave_supports(int64_t m, int64_t topk, int64_t experts, int64_t n, int64_t k, int64_t x_rows);
-hipError_t launch_fused_wave(const Product& p, const Epi& ep, const Rows& rows, int64_t max_tiles,
-                             hipStream_t s);
+hipError_t launch_fused_wave(const Product& p, const Epi& ep, const Rows& rows, int64_t max_tiles, Queue q);
 
 // Dense products of few rows and few row tiles (bf16 x, xb, as it is).
 bool fused_split_supports(int64_t m, int64_t nout, int64_t n, int64_t k, bool xb);
-hipError_t launch_fused_split(const Product& p, const Epi& ep, hipStream_t s);
+hipError_t launch_fused_split(const Product& p, const Epi& ep, Queue q);
 
 struct RouteArgs {
   const void* logits;
@@ -231,6 +249,6 @@ hipError_t launch_route_plan(const int* ids, int64_t m, int64_t topk, int64_t ex
 
 // An expert layer of one token (r.plan unused; up.ep.y is down.x).
 bool moe_one_supports(const RouteArgs& r, const Product& up, const Product& down);
-hipError_t launch_moe_one(const RouteArgs& r, const Product& up, const Product& down, hipStream_t s);
+hipError_t launch_moe_one(const RouteArgs& r, const Product& up, const Product& down, Queue q);
 
 }  // namespace q4

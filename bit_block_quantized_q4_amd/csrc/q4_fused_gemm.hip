@@ -414,10 +414,10 @@ KernelFn kernel_in(Tile t, int mode) {
 
 hipError_t launch_tiles(KernelFn fn, int tile, int threads, const half_t* x, const uint8_t* W, int64_t k,
                         int kps, const FusedArgs& a0, int64_t cols, int64_t row_tiles, int splits,
-                        const void* xe, int xet, hipStream_t s) {
+                        const void* xe, int xet, Queue q) {
   FusedArgs a = a0;
   void* argv[] = {&x, &W, &k, &kps, &a, &xe, &xet};
-  return launch_blocks(fn, (cols + tile - 1) / tile, threads, argv, 0, s, row_tiles, splits);
+  return launch_blocks(fn, (cols + tile - 1) / tile, threads, argv, 0, q, row_tiles, splits);
 }
 
 }  // namespace
@@ -427,17 +427,16 @@ size_t stage_bytes(int64_t rows, int64_t k) {
 }
 
 hipError_t launch_stage(const void* x, int64_t rows, int64_t k, void* ws, const half_t** xs,
-                        const float** scale, hipStream_t s) {
+                        const float** scale, Queue q) {
   const uint16_t* src = static_cast<const uint16_t*>(x);
   uint16_t* dst = static_cast<uint16_t*>(ws);
-  float* inv = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
-                                        up256(static_cast<size_t>(rows) * static_cast<size_t>(k) * 2));
+  float* inv = reinterpret_cast<float*>(behind(ws, up256(static_cast<size_t>(rows) * static_cast<size_t>(k) * 2)));
   *xs = reinterpret_cast<const half_t*>(dst);
   *scale = inv;
   void* argv[] = {&src, &dst, &inv, &rows, &k};
   if (k > kStagePieces * kWave * 8)
-    return launch_blocks(reinterpret_cast<const void*>(&stage_bf16_kernel<true>), rows, 256, argv, 0, s);
-  return launch_blocks(reinterpret_cast<const void*>(&stage_bf16_kernel<false>), (rows + 3) / 4, 256, argv, 0, s);
+    return launch_blocks(reinterpret_cast<const void*>(&stage_bf16_kernel<true>), rows, 256, argv, 0, q);
+  return launch_blocks(reinterpret_cast<const void*>(&stage_bf16_kernel<false>), (rows + 3) / 4, 256, argv, 0, q);
 }
 
 size_t fused_gemm_bytes(int64_t m, int64_t n, int64_t k, DType xt, bool gated, bool grouped) {
@@ -446,8 +445,8 @@ size_t fused_gemm_bytes(int64_t m, int64_t n, int64_t k, DType xt, bool gated, b
 }
 
 hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
-                             const float* xscale, int64_t row_tiles, void* workspace, hipStream_t s) {
-  const bool gated = ep.half != 0, grouped = rows.recs != nullptr;
+                             const float* xscale, int64_t row_tiles, void* workspace, Queue q) {
+  const bool gated = ep.half != 0, grouped = p.experts != 0;
   FusedArgs a{ep, rows, xscale, p.m, tile_cols(p.n, gated), 0, nullptr, 0, 0, 1};
   const int xet = static_cast<int>(p.xt);
   const int plan_rows = grouped ? plan_layout(p.m, p.topk, p.experts).tile_rows : 128;
@@ -461,7 +460,7 @@ hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, 
               : (grouped ? reinterpret_cast<KernelFn>(&fused_exact_kernel<false, kGrouped>)
                          : reinterpret_cast<KernelFn>(&fused_exact_kernel<false, kDense>));
     return launch_tiles(fn, 128, 256, xs, p.W, p.k, 0, a, a.cols, grouped ? row_tiles : (p.m + 127) / 128, 1,
-                        p.x, xet, s);
+                        p.x, xet, q);
   }
   if (p.k % kBK != 0) {
     const KernelFn fn =
@@ -470,7 +469,7 @@ hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, 
               : (grouped ? reinterpret_cast<KernelFn>(&fused_tile_kernel<false, kGrouped>)
                          : reinterpret_cast<KernelFn>(&fused_tile_kernel<false, kDense>));
     return launch_tiles(fn, 128, 256, xs, p.W, p.k, 0, a, a.cols, grouped ? row_tiles : (p.m + 127) / 128, 1,
-                        p.x, xet, s);
+                        p.x, xet, q);
   }
   const int nks = static_cast<int>(p.k / kBK);
   if (grouped) {
@@ -479,10 +478,10 @@ hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, 
       a.parts = 1;
       return launch_tiles(gated ? reinterpret_cast<KernelFn>(&fused_group_kernel<true>)
                                 : reinterpret_cast<KernelFn>(&fused_group_kernel<false>),
-                          256, 512, xs, p.W, p.k, nks, a, a.cols, row_tiles, 1, p.x, xet, s);
+                          256, 512, xs, p.W, p.k, nks, a, a.cols, row_tiles, 1, p.x, xet, q);
     }
     return launch_tiles(gated ? kernel_in<true>(Tile::Out128, mode) : kernel_in<false>(Tile::Out128, mode), 128,
-                        256, xs, p.W, p.k, nks, a, a.cols, row_tiles, 1, p.x, xet, s);
+                        256, xs, p.W, p.k, nks, a, a.cols, row_tiles, 1, p.x, xet, q);
   }
   const GemmPlan g = gemm_plan(p.m, a.cols, p.k, slice_k(p.n, p.k, gated));
   auto threads = [](Tile t) { return t == Tile::Big ? 512 : 256; };
@@ -492,7 +491,7 @@ hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, 
     FusedArgs b = a;
     const int64_t cols = g.n_main < a.cols ? g.n_main : a.cols;
     e = launch_tiles(gated ? kernel_in<true>(g.main, kDense) : kernel_in<false>(g.main, kDense), bt,
-                     threads(g.main), xs, p.W, p.k, nks, b, cols, (p.m + bt - 1) / bt, 1, p.x, xet, s);
+                     threads(g.main), xs, p.W, p.k, nks, b, cols, (p.m + bt - 1) / bt, 1, p.x, xet, q);
     if (e != hipSuccess || g.n_main == a.cols) return e;
   }
   const int bt = tile_rows(g.tail);
@@ -501,14 +500,14 @@ hipError_t launch_fused_gemm(const Product& p, const Epi& ep, const Rows& rows, 
   a.ldp = a.cols - g.n_main;
   a.zstride = p.m * a.ldp;
   e = launch_tiles(gated ? kernel_in<true>(g.tail, kPart) : kernel_in<false>(g.tail, kPart), bt,
-                   threads(g.tail), xs, p.W, p.k, g.kps, a, a.ldp, (p.m + bt - 1) / bt, g.splits, p.x, xet, s);
+                   threads(g.tail), xs, p.W, p.k, g.kps, a, a.ldp, (p.m + bt - 1) / bt, g.splits, p.x, xet, q);
   if (e != hipSuccess) return e;
   int splits = g.splits;
   int64_t quads = (gated ? a.ldp / 2 : a.ldp) / 4;
   void* argv[] = {&a, &splits, &quads};
   const KernelFn fn = gated ? reinterpret_cast<KernelFn>(&fused_reduce_kernel<true>)
                             : reinterpret_cast<KernelFn>(&fused_reduce_kernel<false>);
-  return launch_blocks(fn, (p.m * quads + 255) / 256, 256, argv, 0, s);
+  return launch_blocks(fn, (p.m * quads + 255) / 256, 256, argv, 0, q);
 }
 
 }  // namespace q4

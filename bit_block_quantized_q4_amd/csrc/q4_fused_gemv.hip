@@ -415,8 +415,8 @@ bool fused_gemv_supports(int64_t n, int64_t k, int64_t x_rows, int64_t experts) 
 }
 
 hipError_t launch_fused_gemv(const Product& p, const Epi& ep, const Rows& rows, const half_t* xs,
-                             const float* xscale, int64_t max_tiles, int tile_rows, hipStream_t s) {
-  const bool gated = ep.half != 0, grouped = rows.recs != nullptr;
+                             const float* xscale, int64_t max_tiles, int tile_rows, Queue q) {
+  const bool gated = ep.half != 0, grouped = p.experts != 0;
   const int64_t pairs = p.m * p.topk;
   const int at = (grouped ? tile_rows : p.m) > 16 ? 2 : 1;
   const int64_t tiles = grouped ? (pairs < p.experts ? pairs : p.experts) : 1;
@@ -427,13 +427,12 @@ hipError_t launch_fused_gemv(const Product& p, const Epi& ep, const Rows& rows, 
   if (a.cols < 1) return hipErrorInvalidValue;
   a.cblocks = static_cast<int>((a.nout + a.cols - 1) / a.cols);
   const KernelFn fn = f.form.fn[gated ? 1 : 0];
-  const hipError_t e = allow_dynamic_lds(fn, kTLdsMax, f.form.allowed[gated ? 1 : 0]);
-  if (e != hipSuccess) return e;
   const uint8_t* W = p.W;
   int64_t k = p.k;
   void* argv[] = {&xs, &W, &k, &a};
   const int64_t grid = static_cast<int64_t>(a.cblocks) * (grouped ? max_tiles : 1);
-  return launch_blocks(fn, grid, f.form.threads, argv, static_cast<size_t>(f.form.lds), s);
+  return launch_blocks(fn, grid, f.form.threads, argv, static_cast<size_t>(f.form.lds), q, 1, 1, kTLdsMax,
+                       &f.form.allowed[gated ? 1 : 0]);
 }
 
 }  // namespace q4

@@ -209,7 +209,7 @@ int lds_bytes(int cap, int64_t k, int nw, int ring, bool shift) {
 
 template <int NW, int R>
 hipError_t launch_form(const half_t* x, bool xb, const uint8_t* W, int64_t k, WaveArgs a, bool gated,
-                       bool shift, int lds, int64_t grid, hipStream_t s) {
+                       bool shift, int lds, int64_t grid, Queue q) {
   static const KernelFn fns[8] = {
       reinterpret_cast<KernelFn>(&fused_wave_kernel<NW, R, false, false, false>),
       reinterpret_cast<KernelFn>(&fused_wave_kernel<NW, R, false, false, true>),
@@ -221,10 +221,8 @@ hipError_t launch_form(const half_t* x, bool xb, const uint8_t* W, int64_t k, Wa
       reinterpret_cast<KernelFn>(&fused_wave_kernel<NW, R, true, true, true>)};
   static std::atomic<uint64_t> allowed[8];
   const int f = (gated ? 4 : 0) + (shift ? 2 : 0) + (xb ? 1 : 0);
-  const hipError_t e = allow_dynamic_lds(fns[f], kLdsMax, allowed[f]);
-  if (e != hipSuccess) return e;
   void* argv[] = {&x, &W, &k, &a};
-  return launch_blocks(fns[f], grid, NW * kWave, argv, static_cast<size_t>(lds), s);
+  return launch_blocks(fns[f], grid, NW * kWave, argv, static_cast<size_t>(lds), q, 1, 1, kLdsMax, &allowed[f]);
 }
 
 }  // namespace
@@ -237,7 +235,7 @@ bool fused_wave_supports(int64_t m, int64_t topk, int64_t experts, int64_t n, in
 }
 
 hipError_t launch_fused_wave(const Product& p, const Epi& ep, const Rows& rows, int64_t max_tiles,
-                             hipStream_t s) {
+                             Queue q) {
   const bool gated = ep.half != 0, shift = p.k % 256 != 0, xb = p.xt == DType::BF16;
   const int64_t pairs = p.m * p.topk, cu = device_cu_count();
   WaveArgs a{ep, rows, ep.ldy, 1, cap_rows(p.m)};
@@ -270,14 +268,14 @@ hipError_t launch_fused_wave(const Product& p, const Epi& ep, const Rows& rows, 
   // two chunks, which do not cover the memory's latency).
   if (reached * row_tiles <= 4 * cu && lds(4, 4) <= kLdsMax / 2) {
     const int64_t n = grid(4, 2);
-    return launch_form<4, 4>(x, xb, p.W, p.k, a, gated, shift, lds(4, 4), n, s);
+    return launch_form<4, 4>(x, xb, p.W, p.k, a, gated, shift, lds(4, 4), n, q);
   }
   if (lds(12, 3) <= kLdsMax) {
     const int64_t n = grid(12, 1);
-    return launch_form<12, 3>(x, xb, p.W, p.k, a, gated, shift, lds(12, 3), n, s);
+    return launch_form<12, 3>(x, xb, p.W, p.k, a, gated, shift, lds(12, 3), n, q);
   }
   const int64_t n = grid(8, 1);
-  return launch_form<8, 3>(x, xb, p.W, p.k, a, gated, shift, lds(8, 3), n, s);
+  return launch_form<8, 3>(x, xb, p.W, p.k, a, gated, shift, lds(8, 3), n, q);
 }
 
 // Up to eight rows (fp16) or four (bf16, whose rows every wavefront turns into
@@ -293,7 +291,7 @@ bool fused_split_supports(int64_t m, int64_t nout, int64_t n, int64_t k, bool xb
   return split_lds(m, k, split_waves(k)) <= (tiles <= cu ? kLdsMax : kLdsMax / 2);
 }
 
-hipError_t launch_fused_split(const Product& p, const Epi& ep, hipStream_t s) {
+hipError_t launch_fused_split(const Product& p, const Epi& ep, Queue q) {
   static const KernelFn fns[8] = {reinterpret_cast<KernelFn>(&fused_split_kernel<false, false, false>),
                                   reinterpret_cast<KernelFn>(&fused_split_kernel<false, false, true>),
                                   reinterpret_cast<KernelFn>(&fused_split_kernel<false, true, false>),
@@ -305,8 +303,6 @@ hipError_t launch_fused_split(const Product& p, const Epi& ep, hipStream_t s) {
   static std::atomic<uint64_t> allowed[8];
   const bool gated = ep.half != 0;
   const int f = (gated ? 4 : 0) + (p.k % 256 != 0 ? 2 : 0) + (p.xt == DType::BF16 ? 1 : 0);
-  const hipError_t e = allow_dynamic_lds(fns[f], kLdsMax, allowed[f]);
-  if (e != hipSuccess) return e;
   const int waves = split_waves(p.k);
   const half_t* x = static_cast<const half_t*>(p.x);
   const uint8_t* W = p.W;
@@ -314,7 +310,7 @@ hipError_t launch_fused_split(const Product& p, const Epi& ep, hipStream_t s) {
   SplitArgs a{ep, static_cast<int>(p.m)};
   void* argv[] = {&x, &W, &k, &a};
   return launch_blocks(fns[f], (ep.ldy + (gated ? 7 : 15)) / (gated ? 8 : 16), waves * kWave, argv,
-                       static_cast<size_t>(split_lds(p.m, p.k, waves)), s);
+                       static_cast<size_t>(split_lds(p.m, p.k, waves)), q, 1, 1, kLdsMax, &allowed[f]);
 }
 
 }  // namespace q4

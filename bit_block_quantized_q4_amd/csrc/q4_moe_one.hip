@@ -163,10 +163,8 @@ int down_tiles(int64_t nout) {
 }
 
 hipError_t launch(KernelFn fn, std::atomic<uint64_t>& allowed, int64_t grid, int threads, int lds, void** argv,
-                  hipStream_t s) {
-  const hipError_t e = allow_dynamic_lds(fn, kLdsMax, allowed);
-  if (e != hipSuccess) return e;
-  return launch_blocks(fn, grid, threads, argv, static_cast<size_t>(lds), s);
+                  Queue q) {
+  return launch_blocks(fn, grid, threads, argv, static_cast<size_t>(lds), q, 1, 1, kLdsMax, &allowed);
 }
 
 template <typename K>
@@ -193,7 +191,7 @@ bool moe_one_supports(const RouteArgs& r, const Product& up, const Product& down
          down_lds(down.k, down.k % 256 != 0, r.topk, down_tiles(down.n)) <= kLdsMax;
 }
 
-hipError_t launch_moe_one(const RouteArgs& r, const Product& up, const Product& down, hipStream_t s) {
+hipError_t launch_moe_one(const RouteArgs& r, const Product& up, const Product& down, Queue q) {
   const bool xb = up.xt == DType::BF16, gated = up.ep.half != 0;
   const int64_t cu = device_cu_count();
   {
@@ -213,7 +211,7 @@ hipError_t launch_moe_one(const RouteArgs& r, const Product& up, const Product& 
     const int at = (sums ? 8 : 0) + (gated ? 4 : 0) + (shift ? 2 : 0) + (xb ? 1 : 0);
     const hipError_t e =
         launch(sums ? up_kernel<uint64_t>(gated, shift, xb) : up_kernel<uint32_t>(gated, shift, xb), allowed[at],
-               r.topk * a.parts, kUpWaves * kWave, up_lds(k, shift), argv, s);
+               r.topk * a.parts, kUpWaves * kWave, up_lds(k, shift), argv, q);
     if (e != hipSuccess) return e;
   }
   const bool shift = down.k % 256 != 0;
@@ -229,7 +227,7 @@ hipError_t launch_moe_one(const RouteArgs& r, const Product& up, const Product& 
   static std::atomic<uint64_t> allowed[4];
   const int64_t grid = ((down.n + 15) / 16 + a.tiles - 1) / a.tiles;
   return launch(fn, allowed[(shift ? 2 : 0) + (xb ? 1 : 0)], grid, static_cast<int>(r.topk) * kWave,
-                down_lds(k, shift, r.topk, a.tiles), argv, s);
+                down_lds(k, shift, r.topk, a.tiles), argv, q);
 }
 
 }  // namespace q4

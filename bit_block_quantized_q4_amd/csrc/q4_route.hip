@@ -348,7 +348,7 @@ hipError_t launch_route_plan(const int* ids, int64_t m, int64_t topk, int64_t ex
   const int64_t chunks = (m * topk + kThreads - 1) / kThreads, cu = device_cu_count();
   int span = static_cast<int>((chunks + cu - 1) / cu) * kThreads;
   void* argl[] = {&ids, &pairs, &ne, &span, &L, &plan};
-  return launch_blocks(reinterpret_cast<const void*>(&plan_kernel), (pairs + span - 1) / span, kThreads, argl, 0, s);
+  return launch_blocks(reinterpret_cast<const void*>(&plan_kernel), (pairs + span - 1) / span, kThreads, argl, 0, Queue{s});
 }
 
 }  // namespace q4

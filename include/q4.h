@@ -184,7 +184,9 @@ q4_status q4_gemm_noalloc(const void *x, int x_dtype, const void *packed, void *
  * ------------------------------------------------------------------------
  * The calls below also write Q4_BF16 outputs and take any m >= 1 (one entry
  * for decode and prefill).  Conventions are those at the top of this header
- * except where stated. */
+ * except where stated.  A call with a launch that a grid does not hold (more
+ * than 65535 tiles of 128 to 256 rows, or 2^32 threads) is refused with
+ * Q4_ERR_SHAPE before the first launch, and its workspace size is 0. */
 
 typedef enum q4_activation {
   Q4_ACT_NONE = 0,

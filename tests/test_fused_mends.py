@@ -1,0 +1,44 @@
+"""CPU checks of the fused layers at calls that once went wrong."""
+
+import pytest
+
+from test_fused_abi import A, B, BIG, C, D, E_, F16, F32, BF16, SHAPE, W, ep, routing
+
+
+# ------------------------------------------------------------------ grids
+
+def test_products_that_no_grid_holds_are_refused_before_any_launch(q4lib):
+    """Where a later launch of the call does not fit, the earlier ones (staging, the
+    products before their sum) are not made either: SHAPE, not a failed launch, and
+    no workspace size."""
+    L = q4lib.lib()
+    tall = 1 << 25  # 131072 tiles of 256 rows
+    for dt in (F16, BF16):
+        assert q4lib.q4_linear_workspace_size(tall, 64, 64, dt) == 0
+        assert L.q4_linear(A << 8, dt, B << 8, ep(q4lib), C << 8, dt, tall, 64, 64, W << 8, BIG, None) == SHAPE
+    # 2^24 pairs: 87389 tiles of 192; 2^23 sums of 2560 columns: 3 2^31 threads
+    for m, topk, E, n, combine in ((1 << 21, 8, 8, 64, False), (1 << 21, 8, 8, 64, True), (1 << 23, 1, 1, 2560, True)):
+        for dt in (F16, BF16):
+            rows = m * topk
+            assert q4lib.q4_route_plan_size(m, topk, E) > 0
+            assert q4lib.q4_experts_workspace_size(m, topk, E, n, 64, rows, dt, combine=combine) == 0
+            x, w, p, g, y, ws = (v << 12 for v in (A, B, C, D, E_, W))
+            assert L.q4_experts(x, dt, rows, w, ep(q4lib), p, g if combine else None, y, dt, m, topk, E, n, 64, ws,
+                                BIG, None) == SHAPE
+
+
+@pytest.mark.parametrize("m,topk,hidden,inter", [(1 << 21, 8, 64, 64), (1 << 23, 1, 2560, 64)])
+def test_layers_that_no_grid_holds_are_refused_before_the_routing(q4lib, m, topk, hidden, inter):
+    L, E = q4lib.lib(), 8
+    assert q4lib.q4_moe_workspace_size(m, topk, E, hidden, inter, BF16) == 0
+    x, l, u, d, y, ws = (v << 12 for v in (A, B, C, D, E_, W))
+    args = (x, BF16, l, F32, routing(q4lib), u, ep(q4lib, act=4, gated=1), d, None, y, BF16, m, topk, E, hidden, inter)
+    assert L.q4_moe(*args, None, None, ws, BIG, None) == SHAPE
+    assert L.q4_moe(*args, None, None, None, 0, None) == SHAPE
+
+
+def test_products_that_grids_hold_keep_their_sizes(q4lib):
+    assert q4lib.q4_linear_workspace_size(1 << 23, 64, 64, BF16) >= (1 << 23) * 128
+    assert q4lib.q4_experts_workspace_size(1 << 20, 8, 8, 64, 64, 1 << 20, BF16) >= (1 << 20) * 128
+    assert q4lib.q4_moe_workspace_size(1 << 20, 8, 8, 64, 64, F16) > 0
+    assert q4lib.q4_moe_workspace_size(1, 8, 64, 2048, 768, F16) > 0
