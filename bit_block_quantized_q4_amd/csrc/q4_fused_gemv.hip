@@ -408,9 +408,10 @@ FewPlan few_plan(int m, int64_t n, int64_t k, int64_t tiles, int at) {
 
 bool fused_gemv_supports(int64_t n, int64_t k, int64_t x_rows, int64_t experts) {
   // Whole 16-byte pieces to the end of the packed weights, 32-bit offsets of
-  // a gate's up rows and of x's rows.
+  // a gate's up rows and of x's rows.  (A matrix is reached from the piece that
+  // holds its first byte, up to 12 bytes before it, and to the end of its last.)
   const int64_t rb = k / kQK * kBlockBytes;
-  return k % 64 == 0 && (n * (experts > 0 ? experts : 1) * rb) % 16 == 0 && n * rb < (int64_t{1} << 32) &&
+  return k % 64 == 0 && (n * (experts > 0 ? experts : 1) * rb) % 16 == 0 && n * rb <= (int64_t{1} << 32) - 16 &&
          x_rows * k * 2 < (int64_t{1} << 32);
 }
 

@@ -42,3 +42,17 @@ def test_products_that_grids_hold_keep_their_sizes(q4lib):
     assert q4lib.q4_experts_workspace_size(1 << 20, 8, 8, 64, 64, 1 << 20, BF16) >= (1 << 20) * 128
     assert q4lib.q4_moe_workspace_size(1 << 20, 8, 8, 64, 64, F16) > 0
     assert q4lib.q4_moe_workspace_size(1, 8, 64, 2048, 768, F16) > 0
+
+
+# ------------------------------------------------------------------ 32-bit offsets
+
+def test_matrices_that_end_at_4_gib_leave_the_32_bit_offsets(q4lib):
+    """Rows that fill 2^32 - 4 bytes: an expert that starts 12 bytes into a 16-byte
+    piece reaches its last row by offsets of 2^32 and more from that piece.  The
+    decode kernels, whose offsets have 32 bits, stage bf16 rows; the row kernel, with
+    64, takes them as they are."""
+    n, k = 349867, 21824
+    assert n * (k // 32 * 18) == (1 << 32) - 4
+    size = q4lib.q4_experts_workspace_size
+    assert size(64, 1, 4, n - 1, k, 64, BF16) >= 64 * k * 2
+    assert size(64, 1, 4, n, k, 64, BF16) == 0
