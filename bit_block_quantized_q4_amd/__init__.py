@@ -501,6 +501,14 @@ def _new_plan(m, topk, experts, device):
     return Plan(torch.empty(size // 4, dtype=torch.int32, device=device), m, topk, experts)
 
 
+def _need_plan(plan):
+    """Refuse words that are no plan of the Plan's sizes: the kernels go by them."""
+    size = q4_route_plan_size(plan.m, plan.topk, plan.experts)
+    if plan.words.dtype != _torch().int32 or not size or plan.words.numel() * 4 != size:
+        raise ValueError(f"a plan of {plan.m} tokens, {plan.topk} of {plan.experts} experts is {size // 4} int32 "
+                         f"words; got {plan.words.dtype} {tuple(plan.words.shape)}")
+
+
 def _routing(score, bias, groups, group_topk, group_score, renormalise, scale, experts):
     torch = _torch()
     if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (experts,)):
@@ -610,6 +618,7 @@ def q4_experts(x, packed, plan, bias=None, activation="none", gated=False, weigh
             if out is not None:
                 return out
     torch = _torch()
+    _need_plan(plan)
     index = _same_device(x, packed=packed, bias=bias, plan=plan.words, weights=weights, residual=residual, y=y,
                  workspace=workspace)
     experts, n, k = _expert_shape(packed)

@@ -56,3 +56,23 @@ def test_matrices_that_end_at_4_gib_leave_the_32_bit_offsets(q4lib):
     size = q4lib.q4_experts_workspace_size
     assert size(64, 1, 4, n - 1, k, 64, BF16) >= 64 * k * 2
     assert size(64, 1, 4, n, k, 64, BF16) == 0
+
+
+# ------------------------------------------------------------------ plans
+
+def test_words_that_are_no_plan_of_those_sizes_are_refused(q4lib):
+    """The full way from Python (an output of the caller's) took any words."""
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 64, dtype=torch.float16)
+    packed, y = torch.zeros(8, 32, 36, dtype=torch.uint8), torch.zeros(8, 32, dtype=torch.float16)
+    words = q4lib.q4_route_plan_size(4, 2, 8) // 4
+    for plan in (q4lib.Plan(torch.zeros(3, dtype=torch.int32), 4, 2, 8),
+                 q4lib.Plan(torch.zeros(words, dtype=torch.int64), 4, 2, 8),
+                 q4lib.Plan(torch.zeros(words, dtype=torch.int32), 400, 2, 8),
+                 q4lib.Plan(torch.zeros(0, dtype=torch.int32), 0, 2, 8)):
+        with pytest.raises(ValueError, match="plan of"):
+            q4lib.q4_experts(x, packed, plan, y=y)
+        with pytest.raises(ValueError, match="plan of"):
+            q4lib.q4_experts(x, packed, plan)
+    with pytest.raises(ValueError, match="device tensor"):
+        q4lib.q4_experts(x, packed, q4lib.Plan(torch.zeros(words, dtype=torch.int32), 4, 2, 8), y=y)
