@@ -1,5 +1,8 @@
 """Build libq4.so for gfx950 (and the host-CPU twin libq4host.so) in-tree.
 
+The C library needs hipcc alone.  The native short way from Python to the fused
+calls (_q4_torch.so) is built where torch and its and Python's headers are there.
+
 Usage: ``python -m bit_block_quantized_q4_amd.build`` (or ``build()``).
 Every HIP translation unit is compiled with hipcc for ``--offload-arch=gfx950``
 in parallel, then linked into ``bit_block_quantized_q4_amd/libq4.so``.  The
@@ -13,6 +16,7 @@ import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
+from typing import Optional
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
@@ -90,13 +94,25 @@ def build_host(verbose: bool = False) -> Path:
     return HOST_LIB_PATH
 
 
-def build_torch(verbose: bool = False) -> Path:
+def build_torch(verbose: bool = False) -> Optional[Path]:
     """Compile the fused calls' short way from Python (binding/q4_torch.cpp, host
-    code against torch's headers) into _q4_torch.so; returns its path."""
+    code against torch's headers) into _q4_torch.so; returns its path, or None
+    without torch or the headers: the fused calls then go through ctypes.  (One of
+    an earlier build is removed, it may not fit the library any more.)"""
     import sysconfig
 
-    import torch
-    base = Path(torch.__file__).parent
+    try:
+        import torch
+    except ImportError:
+        torch = None
+    base = Path(torch.__file__).parent if torch is not None else Path()
+    headers = (Path(sysconfig.get_paths()["include"]) / "Python.h", base / "include" / "ATen" / "ATen.h",
+               base / "include" / "c10" / "hip" / "HIPStream.h")
+    missing = ["torch"] if torch is None else [h.name for h in headers if not h.exists()]
+    if missing:
+        TORCH_LIB_PATH.unlink(missing_ok=True)
+        print(f"{TORCH_LIB_PATH.name} is not built, without {', '.join(missing)}", file=sys.stderr, flush=True)
+        return None
     cxx = os.environ.get("CXX", "g++")
     tmp = TORCH_LIB_PATH.with_suffix(".so.tmp")
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
@@ -140,10 +156,9 @@ def build_trace(verbose: bool = False) -> Path:
 
 def build(verbose: bool = False) -> Path:
     """Compile every csrc/*.hip for gfx950 and link libq4.so (and build the
-    host-CPU twin libq4host.so, the torch binding's _q4_torch.so and the benchmark's
-    measurement libq4floor.so); returns libq4.so's path."""
+    host-CPU twin libq4host.so, the benchmark's measurement libq4floor.so and, where
+    torch is there, its binding's _q4_torch.so); returns libq4.so's path."""
     build_host(verbose)
-    build_torch(verbose)
     build_floor(verbose)
     hipcc = _hipcc()
     BUILD_DIR.mkdir(exist_ok=True)
@@ -163,6 +178,7 @@ def build(verbose: bool = False) -> Path:
           *map(str, objs)], verbose)
     os.replace(tmp, LIB_PATH)
     build_trace(verbose)
+    build_torch(verbose)
     return LIB_PATH
 
 
