@@ -142,7 +142,9 @@ def lib() -> ctypes.CDLL:
         except OSError as e:  # pragma: no cover - depends on the host
             raise Q4LibraryMissing(f"cannot load {LIB_PATH}: {e}") from e
         for name, (res, args) in _SIGS.items():
-            fn = getattr(L, name)
+            fn = getattr(L, name, None)
+            if fn is None:  # functions are added within one ABI version
+                raise Q4LibraryMissing(f"{LIB_PATH} has no {name}: it is older than this package; rebuild it")
             fn.restype = res
             fn.argtypes = args
         if L.q4_abi_version() != ABI_VERSION:

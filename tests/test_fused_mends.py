@@ -1,5 +1,8 @@
 """CPU checks of the fused layers at calls that once went wrong."""
 
+import shutil
+import subprocess
+
 import pytest
 
 from test_fused_abi import A, B, BIG, C, D, E_, F16, F32, BF16, SHAPE, W, ep, routing
@@ -76,3 +79,25 @@ def test_words_that_are_no_plan_of_those_sizes_are_refused(q4lib):
             q4lib.q4_experts(x, packed, plan)
     with pytest.raises(ValueError, match="device tensor"):
         q4lib.q4_experts(x, packed, q4lib.Plan(torch.zeros(words, dtype=torch.int32), 4, 2, 8), y=y)
+
+
+# ------------------------------------------------------------------ older libraries
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="gcc not available")
+def test_a_library_older_than_the_binding_is_named_as_such(q4lib, monkeypatch, tmp_path):
+    """One of the same ABI version without the fused calls, and one of another version."""
+    def library(name, functions, version):
+        text = f"int q4_abi_version(void) {{ return {version}; }}\n" + "".join(
+            f"int {f}(void) {{ return 0; }}\n" for f in functions if f != "q4_abi_version")
+        (tmp_path / (name + ".c")).write_text(text)
+        so = tmp_path / (name + ".so")
+        subprocess.run(["gcc", "-shared", "-fPIC", str(tmp_path / (name + ".c")), "-o", str(so)], check=True)
+        return so
+
+    every = list(q4lib._SIGS)
+    monkeypatch.setattr(q4lib, "_LIB", None)
+    for so, match in ((library("old", [f for f in every if f != "q4_moe"], 1), "no q4_moe.*rebuild"),
+                      (library("other", every, 99), "ABI version mismatch")):
+        monkeypatch.setattr(q4lib, "LIB_PATH", so)
+        with pytest.raises(q4lib.Q4LibraryMissing, match=match):
+            q4lib.lib()
