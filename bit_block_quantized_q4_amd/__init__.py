@@ -343,9 +343,21 @@ def _code(table, value, what):
         raise ValueError(f"{what} must be one of {', '.join(table)}; got {value!r}") from None
 
 
+def _need_no_gradient(**tensors):
+    """The fused calls have no gradient: refuse tensors whose results autograd would
+    take for constants."""
+    torch = _torch()
+    for name, t in tensors.items():
+        if t is not None and (t.requires_grad and torch.is_grad_enabled()
+                              or torch.autograd.forward_ad.unpack_dual(t).tangent is not None):
+            raise RuntimeError(f"{name} takes part in a gradient, and this call has none; detach it or call "
+                               "under torch.no_grad()")
+
+
 def _same_device(x, **others):
-    """Refuse host and non-contiguous tensors and tensors of several devices;
-    the device's index."""
+    """Refuse host and non-contiguous tensors, tensors of several devices and ones
+    that take part in a gradient; the device's index."""
+    _need_no_gradient(x=x, **others)
     _need_device(x, "x")
     index = x.get_device()
     for name, t in others.items():
@@ -441,7 +453,8 @@ def q4_linear(x, packed, bias=None, activation="none", gated=False, residual=Non
 
     x [m, k] fp32, fp16 or bf16; packed [n, k/32*18] uint8; bias [n]; residual of
     y's shape and dtype (it may be y itself).  activation: none, relu, gelu (tanh
-    form), gelu_erf or silu.  y defaults to x's dtype."""
+    form), gelu_erf or silu.  y defaults to x's dtype.  None of the fused calls has a
+    gradient: tensors that need one are refused (RuntimeError) unless under no_grad."""
     if stream is not None:
         with _on(stream, x):
             return q4_linear(x, packed, bias, activation, gated, residual, y, y_dtype, workspace)

@@ -3,7 +3,7 @@
 //
 // Each function takes the Python function's arguments by position, checks that
 // the call is an ordinary one (contiguous device tensors of the current device
-// with the right shapes and types), allocates what it returns, and calls the
+// with the right shapes and types, none of them part of a gradient), allocates what it returns, and calls the
 // C entry point, whose address it was given.  It returns None for any other
 // call and for any status but OK (a refused call has launched nothing): the
 // Python function then takes its own full way, with its own errors.
@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -33,6 +34,7 @@ decltype(&q4_moe_workspace_size) p_moe_ws;
 // that fails is remembered.
 struct Call {
   PyObject* const* args;
+  bool grad = at::GradMode::is_enabled();
   bool ok = true;
   int device = -1;
 
@@ -45,7 +47,7 @@ struct Call {
       return nullptr;
     }
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || !t.is_contiguous()) {
+    if (!t.is_cuda() || !t.is_contiguous() || (grad && t.requires_grad()) || t._fw_grad(0).defined()) {
       ok = false;
       return nullptr;
     }

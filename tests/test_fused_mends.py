@@ -101,3 +101,31 @@ def test_a_library_older_than_the_binding_is_named_as_such(q4lib, monkeypatch, t
         monkeypatch.setattr(q4lib, "LIB_PATH", so)
         with pytest.raises(q4lib.Q4LibraryMissing, match=match):
             q4lib.lib()
+
+
+# ------------------------------------------------------------------ gradients
+
+def test_tensors_that_need_a_gradient_are_refused(q4lib):
+    torch = pytest.importorskip("torch")
+    x, r = torch.zeros(4, 64), torch.zeros(4, 8)
+    packed, up, down = (torch.zeros(*s, dtype=torch.uint8) for s in ((8, 36), (8, 64, 36), (8, 64, 18)))
+    logits, plan = torch.zeros(4, 8), q4lib.Plan(torch.zeros(q4lib.q4_route_plan_size(4, 2, 8) // 4,
+                                                             dtype=torch.int32), 4, 2, 8)
+    needs = {n: t.clone().requires_grad_() for n, t in dict(x=x, r=r, logits=logits, bias=torch.zeros(8)).items()}
+    calls = {"x linear": lambda: q4lib.q4_linear(needs["x"], packed),
+             "x full way": lambda: q4lib.q4_linear(needs["x"], packed, y_dtype=torch.float32),
+             "residual": lambda: q4lib.q4_linear(x, packed, residual=needs["r"]),
+             "bias": lambda: q4lib.q4_linear(x, packed, bias=needs["bias"]),
+             "logits": lambda: q4lib.q4_route(needs["logits"], 2),
+             "weights": lambda: q4lib.q4_experts(x, up, plan, weights=torch.zeros(4, 2, requires_grad=True)),
+             "x experts": lambda: q4lib.q4_experts(needs["x"], up, plan),
+             "moe": lambda: q4lib.q4_moe(x, needs["logits"], up, down, 2)}
+    for name, f in calls.items():
+        with pytest.raises(RuntimeError, match="part in a gradient"):
+            f()
+        with torch.no_grad(), pytest.raises(ValueError, match="device tensor"):  # as ever
+            f()
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(x, torch.ones_like(x))
+        with pytest.raises(RuntimeError, match="part in a gradient"):
+            q4lib.q4_linear(dual, packed)
