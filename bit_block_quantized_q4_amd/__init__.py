@@ -343,7 +343,7 @@ def _code(table, value, what):
         raise ValueError(f"{what} must be one of {', '.join(table)}; got {value!r}") from None
 
 
-def _need_no_gradient(**tensors):
+def _need_no_gradient(tensors):
     """The fused calls have no gradient: refuse tensors whose results autograd would
     take for constants."""
     torch = _torch()
@@ -357,7 +357,9 @@ def _need_no_gradient(**tensors):
 def _same_device(x, **others):
     """Refuse host and non-contiguous tensors, tensors of several devices and ones
     that take part in a gradient; the device's index."""
-    _need_no_gradient(x=x, **others)
+    dual = getattr(_torch().autograd.forward_ad, "_current_level", 0) >= 0
+    if dual or x.requires_grad or any([t is not None and t.requires_grad for t in others.values()]):
+        _need_no_gradient({"x": x, **others})  # (its questions take 4 us)
     _need_device(x, "x")
     index = x.get_device()
     for name, t in others.items():
@@ -619,8 +621,9 @@ def q4_experts(x, packed, plan, bias=None, activation="none", gated=False, weigh
 
     x: [m, k] (a token's row goes to all its experts) or [m * topk, k] (row p);
     packed: [experts, n, k/32*18] uint8; bias: [experts, n].  Without `weights` y
-    is [m * topk, nout], and rows of pairs without an expert are left as they
-    were (not written); with weights [m, topk] fp32 y is [m, nout], the weighted
+    is [m * topk, nout], and rows of pairs without an expert are not written, the
+    residual included: a y of the caller's keeps them, one allocated here holds
+    anything in them (a second q4_experts over the plan does not read them); with weights [m, topk] fp32 y is [m, nout], the weighted
     sum over a token's experts.  The residual has y's shape and dtype."""
     if stream is not None:
         with _on(stream, x):
