@@ -49,8 +49,17 @@ struct PlanLayout {
 // expert alone, so that one plan serves every product over it: 16 (one
 // activation tile of the matrix-core decode kernel) up to 12 rows, 32 up to
 // 40, then the 128-row tiles of the prefill kernel, and from 80 on the experts'
-// own tile of 192 rows (128 experts, 128 rows on average, 2048 x 2048 gated:
-// 232 us against 305 us with 128-row tiles; at a mean of 96 the two are equal).
+// own tile of 192 rows.  Tiles of 16 and 32 rows multiply exact codes, the higher
+// ones weights rounded to fp16.  Experts chosen evenly, gated, fp16, us with tiles
+// of 16 / 32 / 128 / 192 rows, device time of the product:
+//   mean          10               14               24               40
+//   128 x 4096 x 2048   240/242/-/-   235/250/387/-   323/274/369/273   380/459/383/284
+//   32 x 4096 x 4096    83/102/-/-    95/105/176/-    144/118/178/132   196/191/180/138
+//   mean          64               80               96               128
+//   128 x 4096 x 2048   -/605/401/338  -/730/411/378  -/856/408/388  -/1080/579/447
+//   32 x 4096 x 4096    -/252/188/165  -/294/189/177  -/340/196/178  -/428/283/211
+// The borders are older than this table: 192 rows take less time than 128 at every
+// mean of it, and than 32 from about 24 to 32 on.
 constexpr int kGroupRows = 192;
 
 inline int expert_tile_rows(int64_t m, int64_t topk, int64_t experts) {

@@ -17,8 +17,9 @@
 //     8 or 12 bytes, is the same in every phase and for every 8th row, so it is
 //     a constant of the lane), and the last phase may be short; its copies and
 //     its waves' blocks stop at the row's end.
-// Ten rows of 5120 against 34816 gated weight rows: 23.7 us, 4.25 TB/s (a large
-// copy moves 4.8).  Narrow layers of few rows: see fused_split_kernel.
+// Ten rows of 5120 against 34816 gated weight rows: 23.7 us a call among others,
+// 4.25 TB/s (a large copy moves 4.8); a traced launch, which overlaps no other,
+// takes 25.7.  Narrow layers of few rows: see fused_split_kernel.
 #include "q4_fused.hpp"
 #include "q4_tile_geo.hpp"
 

@@ -271,7 +271,7 @@ typedef struct q4_routing {
   const float *bias; /* [experts] fp32 device array, 4-byte aligned; NULL: none */
   int groups;        /* 1 .. Q4_MAX_GROUPS, divides experts */
   int group_topk;    /* 1 .. groups */
-  int group_score;   /* q4_group_score; read when groups > 1 */
+  int group_score;   /* q4_group_score; used when groups > 1 */
   int renormalise;   /* 0 or 1 */
   float scale;       /* finite */
 } q4_routing;
@@ -307,7 +307,7 @@ size_t q4_experts_workspace_size(int64_t m, int64_t topk, int64_t experts, int64
  *   row p = act((x_p . dequant(packed[e])^T) + bias[e])   (gated: as above)
  * with x_p = x[i] for x_rows == m and x_p = x[p] for x_rows == m topk.
  *   weights == NULL: y is [m topk][nout], y[p] = row p + residual[p]; a pair
- *     without an expert leaves its row of y as it was.
+ *     without an expert leaves its row of y as it was (no residual either).
  *   weights != NULL (fp32 [m][topk]): y is [m][nout],
  *     y[i] = sum_j weights[i][j] row(i topk + j) + residual[i], summed in fp32
  *     in the order of j; pairs without an expert count 0.
