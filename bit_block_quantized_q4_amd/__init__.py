@@ -359,7 +359,7 @@ def _same_device(x, **others):
     that take part in a gradient; the device's index."""
     dual = getattr(_torch().autograd.forward_ad, "_current_level", 0) >= 0
     if dual or x.requires_grad or any([t is not None and t.requires_grad for t in others.values()]):
-        _need_no_gradient({"x": x, **others})  # (its questions take 4 us)
+        _need_no_gradient({"x": x, **others})  # (1 us if always asked)
     _need_device(x, "x")
     index = x.get_device()
     for name, t in others.items():
