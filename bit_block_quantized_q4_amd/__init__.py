@@ -11,7 +11,8 @@ Functions mirror the C entry points: ``q4_packed_size``,
 ``q4_gemm_workspace_size``, ``q4_gemm_workspace_size_dt``, ``q4_quantize``, ``q4_gemv``, ``q4_gemm``,
 ``q4_gemm_noalloc``, ``q4_status_string``, ``q4_abi_version``; the fused linear
 layer ``q4_linear``; the experts' ``q4_route``, ``q4_route_plan``, ``q4_experts``
-and ``q4_moe``, with their size helpers.
+and ``q4_moe``; the cache of keys and values, ``q4_cache_write`` and
+``q4_cache_read``, and ``q4_attention`` over it, with their size helpers.
 """
 
 from __future__ import annotations
@@ -49,6 +50,9 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORES = {"max": 0, "top2": 1}
 MAX_EXPERTS = 1024
 MAX_TOPK = 32
+CACHE_GRANULE = 16
+CACHE_MAX_HEAD_DIM = 256
+CACHE_MAX_SEQS = 65536
 
 
 class Epilogue(ctypes.Structure):
@@ -63,6 +67,24 @@ class Routing(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int),
                 ("group_topk", ctypes.c_int), ("group_score", ctypes.c_int),
                 ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class CacheArg(ctypes.Structure):
+    """q4_cache."""
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64)]
+
+
+class BatchArg(ctypes.Structure):
+    """q4_batch."""
+    _fields_ = [("seqs", ctypes.c_int64), ("tokens", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("tables", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("offsets", ctypes.c_void_p)]
+
+
+class AttentionOptions(ctypes.Structure):
+    """q4_attention_options."""
+    _fields_ = [("scale", ctypes.c_float), ("causal", ctypes.c_int), ("window", ctypes.c_int64),
+                ("softcap", ctypes.c_float)]
 
 
 _P, _I, _L, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -95,6 +117,11 @@ _SIGS = {
     "q4_experts": (_I, [_P, _I, _L, _P, _P, _P, _P, _P, _I] + [_L] * 5 + [_P, _Z, _P]),
     "q4_moe_workspace_size": (_Z, [_L] * 5 + [_I] * 2),
     "q4_moe": (_I, [_P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I] + [_L] * 5 + [_P, _P, _P, _Z, _P]),
+    "q4_cache_size": (_Z, [_L] * 4),
+    "q4_cache_write": (_I, [_P, _P, _P, _L, _P, _L, _I, _P]),
+    "q4_cache_read": (_I, [_P, _P, _P, _P, _I, _P]),
+    "q4_attention_workspace_size": (_Z, [_L] * 5 + [_I] * 2),
+    "q4_attention": (_I, [_P] * 4 + [_L, _I, _L, _P, _I, _P, _P, _Z, _P]),
 }
 
 
@@ -725,3 +752,185 @@ def q4_moe(x, logits, up, down, topk, activation="silu", gated=True, up_bias=Non
             None if ids is None else ids.data_ptr(), None if weights is None else weights.data_ptr(), wptr,
             wbytes)
     return y
+
+
+# ------------------------------------------------------------ cache and attention
+
+def q4_cache_size(pages: int, page_size: int, kv_heads: int, head_dim: int) -> int:
+    return lib().q4_cache_size(int(pages), int(page_size), int(kv_heads), int(head_dim))
+
+
+def q4_cache(pages, page_size, kv_heads, head_dim, device="cuda"):
+    """An empty cache of keys and values: a uint8 tensor [pages, kv_heads, 2,
+    page_size / 16, 9 * head_dim], which the calls below take (a cache of several
+    layers is one such tensor for each).  page_size is a multiple of 16, head_dim
+    one of 32 up to 256."""
+    if not q4_cache_size(pages, page_size, kv_heads, head_dim):
+        raise Q4Error(Q4_ERR_SHAPE, f"cache of {pages} pages of {page_size} positions, {kv_heads} heads of {head_dim}")
+    return _torch().zeros((pages, kv_heads, 2, page_size // CACHE_GRANULE, 9 * head_dim), dtype=_torch().uint8,
+                          device=device)
+
+
+def _cache_arg(cache):
+    if cache.dtype != _torch().uint8:
+        raise TypeError(f"cache must be uint8; got {cache.dtype}")
+    if cache.dim() != 5 or cache.shape[2] != 2 or cache.shape[4] % (9 * QK):
+        raise ValueError("cache must be [pages, kv_heads, 2, page_size / 16, 9 * head_dim] uint8; "
+                         f"got {tuple(cache.shape)}")
+    pages, kv_heads, _, granules, row = cache.shape
+    return CacheArg(cache.data_ptr(), pages, granules * CACHE_GRANULE, kv_heads, row // 9)
+
+
+def _batch_arg(tables, lengths, offsets, tokens):
+    torch = _torch()
+    for name, t in (("tables", tables), ("lengths", lengths), ("offsets", offsets)):
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32; got {t.dtype}")
+    if tables.dim() != 2 or tuple(lengths.shape) != (tables.shape[0],):
+        raise ValueError(f"tables must be [seqs, max_pages], lengths [seqs]; got {tuple(tables.shape)}, "
+                         f"{tuple(lengths.shape)}")
+    seqs = int(tables.shape[0])
+    if offsets is None:
+        if tokens != seqs:
+            raise ValueError(f"without offsets each of the {seqs} sequences has one row; got {tokens}")
+    elif tuple(offsets.shape) != (seqs + 1,):
+        raise ValueError(f"offsets must be [{seqs + 1}]; got {tuple(offsets.shape)}")
+    return BatchArg(seqs, tokens, tables.shape[1], tables.data_ptr(), lengths.data_ptr(),
+                    None if offsets is None else offsets.data_ptr())
+
+
+def _row_stride(t, name, heads, head_dim):
+    """Elements between the rows of t [tokens, heads, head_dim], whose heads lie together."""
+    if t.dim() != 3 or (heads and t.shape[1] != heads) or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {head_dim}]; got {tuple(t.shape)}")
+    if t.shape[0] > 1 or t.stride(0) >= t.shape[1] * head_dim:
+        stride = t.stride(0)
+    else:  # one row: its stride says nothing
+        stride = t.shape[1] * head_dim
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name}'s heads must lie together (only rows may have a stride)")
+    return stride
+
+
+def _same_device_rows(x, rows, **others):
+    """As _same_device, for a call whose x and `rows` may be strided."""
+    for name, t in {"x": x, **rows}.items():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.get_device() != x.get_device():
+            raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+    _need_no_gradient({"x": x, **rows})
+    index = x.get_device()
+    for name, t in others.items():
+        if t is not None:
+            _need_device(t, name)
+            _need_no_gradient({name: t})
+            if t.get_device() != index:
+                raise ValueError(f"{name} is on {t.device}, not on {x.device}")
+    return index
+
+
+def q4_cache_write(k, v, cache, tables, lengths, offsets=None, stream=None):
+    """Quantise rows of keys and values into their places in a paged cache.
+
+    k, v: [tokens, kv_heads, head_dim] fp32, fp16 or bf16; only rows may have a
+    stride (the k and v parts of a fused product's rows).  Sequence s has rows
+    offsets[s] .. offsets[s + 1] - 1 (int32 [seqs + 1]; None: row s alone) and
+    lengths[s] positions (int32 [seqs]), of which its rows are the last; position t
+    lies in page tables[s, t // page_size] (int32 [seqs, max_pages]).  Positions
+    whose page number names no page are left out."""
+    if stream is not None:
+        with _on(stream, k):
+            return q4_cache_write(k, v, cache, tables, lengths, offsets)
+    index = _same_device_rows(k, {"v": v}, cache=cache, tables=tables, lengths=lengths, offsets=offsets)
+    c = _cache_arg(cache)
+    ks, vs = _row_stride(k, "k", c.kv_heads, c.head_dim), _row_stride(v, "v", c.kv_heads, c.head_dim)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError(f"k and v must be alike; got {tuple(k.shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
+    b = _batch_arg(tables, lengths, offsets, int(k.shape[0]))
+    _launch(index, "q4_cache_write", lib().q4_cache_write, ctypes.byref(c), ctypes.byref(b), k.data_ptr(), ks,
+            v.data_ptr(), vs, _dtype_code(k))
+
+
+def q4_cache_read(cache, tables, lengths, offsets=None, tokens=None, dtype=None, k=None, v=None, stream=None):
+    """The decoded keys and values of the rows' positions: (k, v), each [tokens,
+    kv_heads, head_dim] of `dtype` (default fp16), or those given.
+
+    The batch is q4_cache_write's.  tokens: how many rows there are (offsets[-1],
+    which is on the device; without offsets one a sequence).  Rows of no sequence are
+    not written; rows without a position or a page are zeros."""
+    if stream is not None:
+        with _on(stream, cache):
+            return q4_cache_read(cache, tables, lengths, offsets, tokens, dtype, k, v)
+    torch = _torch()
+    index = _same_device_rows(cache, {}, cache=cache, tables=tables, lengths=lengths, offsets=offsets, k=k, v=v)
+    c = _cache_arg(cache)
+    if tokens is None:
+        given = k if k is not None else v
+        if given is None and offsets is not None:
+            raise ValueError("with offsets, tokens (the number of rows) must be given")
+        tokens = int(given.shape[0] if given is not None else lengths.shape[0])
+    shape = (int(tokens), int(c.kv_heads), int(c.head_dim))
+    if dtype is None:
+        dtype = k.dtype if k is not None else v.dtype if v is not None else torch.float16
+    out = []
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=cache.device)
+        if t.dtype != dtype or tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {dtype} {shape}; got {t.dtype} {tuple(t.shape)}")
+        out.append(t)
+    b = _batch_arg(tables, lengths, offsets, shape[0])
+    _launch(index, "q4_cache_read", lib().q4_cache_read, ctypes.byref(c), ctypes.byref(b), out[0].data_ptr(),
+            out[1].data_ptr(), _dtype_code(out[0]))
+    return out[0], out[1]
+
+
+def q4_attention_workspace_size(seqs: int, tokens: int, heads: int, kv_heads: int, head_dim: int, q_dtype: int,
+                                with_offsets: bool = False) -> int:
+    return lib().q4_attention_workspace_size(int(seqs), int(tokens), int(heads), int(kv_heads), int(head_dim),
+                                             int(q_dtype), int(bool(with_offsets)))
+
+
+def q4_attention(q, cache, tables, lengths, offsets=None, scale=None, causal=True, window=0, softcap=0.0,
+                 return_lse=False, y=None, y_dtype=None, lse=None, workspace=None, stream=None):
+    """Softmax attention of q [tokens, heads, head_dim] over the positions that the
+    sequences have in a paged cache; the batch is q4_cache_write's, which comes first
+    (a row sees its own position through the cache).
+
+    heads is a multiple of the cache's kv heads; only q's rows may have a stride.
+    scale defaults to 1 / sqrt(head_dim).  A row at position p sees the positions of
+    its sequence, with `causal` those up to p, with a window those above p - window;
+    softcap > 0 bends its scores: softcap * tanh(s / softcap).  Returns y [tokens,
+    heads, head_dim] of q's dtype (or y_dtype), with return_lse (y, lse): lse [tokens,
+    heads] fp32, the logarithm of the sum of exp.  A row that sees nothing has y 0, lse
+    -inf; rows of no sequence are not written."""
+    if stream is not None:
+        with _on(stream, q):
+            return q4_attention(q, cache, tables, lengths, offsets, scale, causal, window, softcap, return_lse, y,
+                                y_dtype, lse, workspace)
+    torch = _torch()
+    index = _same_device_rows(q, {}, cache=cache, tables=tables, lengths=lengths, offsets=offsets, y=y, lse=lse,
+                              workspace=workspace)
+    c = _cache_arg(cache)
+    qs = _row_stride(q, "q", 0, c.head_dim)
+    tokens, heads = int(q.shape[0]), int(q.shape[1])
+    b = _batch_arg(tables, lengths, offsets, tokens)
+    y = _full_out(y, (tokens, heads, int(c.head_dim)), _out_dtype(y, y_dtype, q), q.device)
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (tokens, heads)):
+        raise ValueError(f"lse must be float32 {(tokens, heads)}; got {lse.dtype} {tuple(lse.shape)}")
+    if lse is None and return_lse:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+    if int(window) < 0:
+        raise ValueError(f"window must be 0 (none) or more; got {window}")
+    options = AttentionOptions(c.head_dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window),
+                               float(softcap))
+    qd = _dtype_code(q)
+    L = lib()
+    workspace, wptr, wbytes = _workspace(
+        workspace, L.q4_attention_workspace_size(b.seqs, tokens, heads, c.kv_heads, c.head_dim, qd,
+                                                 0 if offsets is None else 1), q.device)
+    _launch(index, "q4_attention", L.q4_attention, ctypes.byref(c), ctypes.byref(b), ctypes.byref(options),
+            q.data_ptr(), qs, qd, heads, y.data_ptr(), _dtype_code(y), None if lse is None else lse.data_ptr(), wptr,
+            wbytes)
+    return (y, lse) if return_lse else y

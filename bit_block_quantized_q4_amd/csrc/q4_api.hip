@@ -4,7 +4,7 @@
 #include <mutex>
 
 #include "q4.h"
-#include "q4_fused.hpp"
+#include "q4_cache.hpp"
 
 // Workspace of q4_gemm_noalloc: one copy per device that loads the library,
 // held until the process ends.  In host code `scratch` names a host-side
@@ -555,6 +555,194 @@ q4_status q4_moe(const void* x, int x_dtype, const void* logits, int logits_dtyp
   if (e == hipSuccess) e = q4::launch_product(p, pw, q);
   if (e == hipSuccess) e = q4::launch_product(d, pw, q);
   return from_hip(e);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ cache and attention
+
+namespace {
+
+constexpr int64_t kMaxPositions = int64_t(1) << 30;  // of one sequence, and of one page
+constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxHeads = 65536;
+
+bool valid_cache(int64_t pages, int64_t page_size, int64_t kv_heads, int64_t head_dim) {
+  return pages >= 1 && pages <= kMaxInt && page_size >= Q4_CACHE_GRANULE && page_size <= kMaxPositions &&
+         page_size % Q4_CACHE_GRANULE == 0 && kv_heads >= 1 && kv_heads < kMaxHeads && head_dim >= Q4_QK &&
+         head_dim <= Q4_CACHE_MAX_HEAD_DIM && head_dim % Q4_QK == 0 &&
+         pages <= kMaxElems / (page_size * head_dim) / kv_heads;
+}
+
+bool valid_rows(int64_t seqs, int64_t tokens) {
+  return seqs >= 1 && seqs <= Q4_CACHE_MAX_SEQS && tokens >= 1 && tokens <= kMaxInt;
+}
+
+// What every call asks of its cache and batch.
+q4_status check_cache(const q4_cache* c, const q4_batch* b) {
+  if (!c || !b || !c->data || !b->tables || !b->lengths) return Q4_ERR_INVALID_ARG;
+  if (!valid_cache(c->pages, c->page_size, c->kv_heads, c->head_dim) || !valid_rows(b->seqs, b->tokens) ||
+      (!b->offsets && b->tokens != b->seqs) || b->max_pages < 1 || b->max_pages > kMaxPositions / c->page_size)
+    return Q4_ERR_SHAPE;
+  return Q4_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool aligned_batch(const q4_cache* c, const q4_batch* b) {
+  return aligned16(c->data) && aligned4(b->tables) && aligned4(b->lengths) && aligned4(b->offsets);
+}
+
+// Rows of `width` elements, `stride` elements apart.
+q4_status check_rows(const void* p, int64_t rows, int64_t width, int64_t stride, int dtype, Span* span) {
+  if (stride < width || stride > kMaxElems || rows > kMaxElems / stride) return Q4_ERR_SHAPE;
+  if (!valid_in_dtype(dtype)) return Q4_ERR_DTYPE;
+  const size_t size = dtype_bytes(dtype);
+  if (!aligned16(p) || static_cast<size_t>(stride) * size % 16 != 0) return Q4_ERR_ALIGNMENT;
+  *span = {p, (static_cast<size_t>(rows - 1) * stride + width) * size};
+  return Q4_OK;
+}
+
+Span cache_span(const q4_cache* c) {
+  return {c->data, q4_cache_size(c->pages, c->page_size, c->kv_heads, c->head_dim)};
+}
+Span tables_span(const q4_batch* b) { return {b->tables, static_cast<size_t>(b->seqs) * b->max_pages * 4}; }
+Span lengths_span(const q4_batch* b) { return {b->lengths, static_cast<size_t>(b->seqs) * 4}; }
+Span offsets_span(const q4_batch* b) { return {b->offsets, b->offsets ? static_cast<size_t>(b->seqs + 1) * 4 : 0}; }
+
+q4::Cache device_cache(const q4_cache* c) {
+  return q4::make_cache(c->data, c->pages, c->page_size, c->kv_heads, c->head_dim);
+}
+q4::Batch device_batch(const q4_cache* c, const q4_batch* b) {
+  q4::Batch d;
+  d.tables = b->tables;
+  d.lengths = b->lengths;
+  d.offsets = b->offsets;
+  d.seqs = static_cast<int>(b->seqs);
+  d.tokens = static_cast<int>(b->tokens);
+  d.max_pages = static_cast<int>(b->max_pages);
+  d.max_length = static_cast<int>(b->max_pages * c->page_size);
+  return d;
+}
+
+bool valid_heads(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim) {
+  return heads >= 1 && heads <= kMaxHeads && kv_heads >= 1 && heads % kv_heads == 0 &&
+         tokens <= kMaxElems / (heads * head_dim);
+}
+
+constexpr q4::Queue kDry{nullptr, true};
+
+}  // namespace
+
+extern "C" {
+
+size_t q4_cache_size(int64_t pages, int64_t page_size, int64_t kv_heads, int64_t head_dim) {
+  if (!valid_cache(pages, page_size, kv_heads, head_dim)) return 0;
+  return static_cast<size_t>(pages) * page_size * kv_heads * 2 * (head_dim / Q4_QK) * Q4_BLOCK_BYTES;
+}
+
+q4_status q4_cache_write(const q4_cache* cache, const q4_batch* batch, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, int dtype, q4_stream_t stream) {
+  if (!k || !v) return Q4_ERR_INVALID_ARG;
+  q4_status st = check_cache(cache, batch);
+  if (st != Q4_OK) return st;
+  const int64_t width = cache->kv_heads * cache->head_dim;
+  Span ks, vs;
+  if ((st = check_rows(k, batch->tokens, width, k_stride, dtype, &ks)) != Q4_OK) return st;
+  if ((st = check_rows(v, batch->tokens, width, v_stride, dtype, &vs)) != Q4_OK) return st;
+  if (!aligned_batch(cache, batch)) return Q4_ERR_ALIGNMENT;
+  if (overlaps_any(cache_span(cache), {ks, vs, tables_span(batch), lengths_span(batch), offsets_span(batch)}))
+    return Q4_ERR_INVALID_ARG;
+  const q4::Cache c = device_cache(cache);
+  const q4::Batch b = device_batch(cache, batch);
+  const q4::DType dt = static_cast<q4::DType>(dtype);
+  if (q4::launch_cache_write(c, b, k, k_stride, v, v_stride, dt, kDry) != hipSuccess) return Q4_ERR_SHAPE;
+  return from_hip(q4::launch_cache_write(c, b, k, k_stride, v, v_stride, dt,
+                                         q4::Queue{reinterpret_cast<hipStream_t>(stream)}));
+}
+
+q4_status q4_cache_read(const q4_cache* cache, const q4_batch* batch, void* k, void* v, int dtype,
+                        q4_stream_t stream) {
+  if (!k || !v) return Q4_ERR_INVALID_ARG;
+  q4_status st = check_cache(cache, batch);
+  if (st != Q4_OK) return st;
+  const int64_t width = cache->kv_heads * cache->head_dim;
+  Span ks, vs;
+  if ((st = check_rows(k, batch->tokens, width, width, dtype, &ks)) != Q4_OK) return st;
+  if ((st = check_rows(v, batch->tokens, width, width, dtype, &vs)) != Q4_OK) return st;
+  if (!aligned_batch(cache, batch)) return Q4_ERR_ALIGNMENT;
+  const Span cs = cache_span(cache), ts = tables_span(batch), ls = lengths_span(batch), os = offsets_span(batch);
+  if (overlaps_any(ks, {vs, cs, ts, ls, os}) || overlaps_any(vs, {cs, ts, ls, os})) return Q4_ERR_INVALID_ARG;
+  const q4::Cache c = device_cache(cache);
+  const q4::Batch b = device_batch(cache, batch);
+  const q4::DType dt = static_cast<q4::DType>(dtype);
+  if (q4::launch_cache_read(c, b, k, v, dt, kDry) != hipSuccess) return Q4_ERR_SHAPE;
+  return from_hip(q4::launch_cache_read(c, b, k, v, dt, q4::Queue{reinterpret_cast<hipStream_t>(stream)}));
+}
+
+size_t q4_attention_workspace_size(int64_t seqs, int64_t tokens, int64_t heads, int64_t kv_heads,
+                                   int64_t head_dim, int q_dtype, int with_offsets) {
+  if (!valid_rows(seqs, tokens) || !valid_cache(1, Q4_CACHE_GRANULE, kv_heads, head_dim) ||
+      !valid_heads(tokens, heads, kv_heads, head_dim) || !valid_in_dtype(q_dtype) || with_offsets < 0 ||
+      with_offsets > 1 || (!with_offsets && tokens != seqs))
+    return 0;
+  q4::Attention a;
+  a.cache.kv_heads = static_cast<int>(kv_heads);
+  a.cache.dim = static_cast<int>(head_dim);
+  a.batch.seqs = static_cast<int>(seqs);
+  a.batch.tokens = static_cast<int>(tokens);
+  const int some = 0;
+  a.batch.offsets = with_offsets ? &some : nullptr;  // (asked for being there alone)
+  a.heads = static_cast<int>(heads);
+  a.group = static_cast<int>(heads / kv_heads);
+  a.qt = static_cast<q4::DType>(q_dtype);
+  if (q4::launch_attention(a, nullptr, kDry) != hipSuccess) return 0;
+  return q4::attention_workspace_bytes(a);
+}
+
+q4_status q4_attention(const q4_cache* cache, const q4_batch* batch, const q4_attention_options* options,
+                       const void* q, int64_t q_stride, int q_dtype, int64_t heads, void* y, int y_dtype,
+                       float* lse, void* workspace, size_t workspace_bytes, q4_stream_t stream) {
+  if (!options || !q || !y) return Q4_ERR_INVALID_ARG;
+  q4_status st = check_cache(cache, batch);
+  if (st != Q4_OK) return st;
+  if (!valid_heads(batch->tokens, heads, cache->kv_heads, cache->head_dim)) return Q4_ERR_SHAPE;
+  if (!(fabsf(options->scale) <= 3.4028234e38f) || !(options->softcap >= 0.f && options->softcap <= 3.4028234e38f) ||
+      options->causal < 0 || options->causal > 1 || options->window < 0)
+    return Q4_ERR_INVALID_ARG;
+  Span qs, ys;
+  const int64_t width = heads * cache->head_dim;
+  if ((st = check_rows(q, batch->tokens, width, q_stride, q_dtype, &qs)) != Q4_OK) return st;
+  if ((st = check_rows(y, batch->tokens, width, width, y_dtype, &ys)) != Q4_OK) return st;
+  if (!aligned_batch(cache, batch) || !aligned16(lse)) return Q4_ERR_ALIGNMENT;
+  const Span es{lse, static_cast<size_t>(batch->tokens) * heads * 4};
+  const Span cs = cache_span(cache), ts = tables_span(batch), ls = lengths_span(batch), os = offsets_span(batch);
+  if (overlaps_any(ys, {qs, es, cs, ts, ls, os}) || overlaps_any(es, {qs, cs, ts, ls, os}))
+    return Q4_ERR_INVALID_ARG;
+  q4::Attention a;
+  a.cache = device_cache(cache);
+  a.batch = device_batch(cache, batch);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.qt = static_cast<q4::DType>(q_dtype);
+  a.heads = static_cast<int>(heads);
+  a.group = static_cast<int>(heads / cache->kv_heads);
+  a.scale = options->scale;
+  a.softcap = options->softcap;
+  a.causal = options->causal;
+  // A window of every position that there can be is none.
+  a.window = options->window > kMaxPositions ? 0 : static_cast<int>(options->window);
+  a.y = y;
+  a.y_dt = y_dtype;
+  a.lse = lse;
+  if (q4::launch_attention(a, nullptr, kDry) != hipSuccess) return Q4_ERR_SHAPE;
+  const size_t need = q4::attention_workspace_bytes(a);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return Q4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q4_ERR_ALIGNMENT;
+    if (overlaps_any({workspace, need}, {qs, ys, es, cs, ts, ls, os})) return Q4_ERR_INVALID_ARG;
+  }
+  return from_hip(q4::launch_attention(a, workspace, q4::Queue{reinterpret_cast<hipStream_t>(stream)}));
 }
 
 }  // extern "C"

@@ -19,7 +19,7 @@
 // one residual step decides every code whose t is not within 2^-16 of an
 // integer, the rest redo the IEEE division (the library is built without
 // fast-math).
-#include "q4_internal.hpp"
+#include "q4_quantize_block.hpp"
 
 namespace q4 {
 namespace {
@@ -65,91 +65,14 @@ struct Load4<half_t> {
   }
 };
 
-// Lane exchange inside a group of eight (DPP, no LDS round trip).
-constexpr int kDppXor1 = 0xB1;      // quad_perm [1, 0, 3, 2]
-constexpr int kDppXor2 = 0x4E;      // quad_perm [2, 3, 0, 1]
-constexpr int kDppHalfMirror = 0x141;  // lane i <-> 7 - i within each 8 lanes
-constexpr int kDppShl4 = 0x104;     // lane i reads lane i + 4 (row_shl:4)
-
-template <int CTRL>
-__device__ __forceinline__ int dpp_i(int v) {
-  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp_f(float v) {
-  return __builtin_bit_cast(float, dpp_i<CTRL>(__builtin_bit_cast(int, v)));
-}
-
-// Keep the (value, index) of larger magnitude, the smaller index on a tie.
-template <int CTRL>
-__device__ __forceinline__ void amax_step(float& best, float& bmag, int& bidx) {
-  const float ob = dpp_f<CTRL>(best);
-  const int oi = dpp_i<CTRL>(bidx);
-  const float om = fabsf(ob);
-  if (om > bmag || (om == bmag && oi < bidx)) { best = ob; bmag = om; bidx = oi; }
-}
-
-// Code q = min(15, trunc(fl(fl(x / D) + 8.5))) (negative truncations clamp to
-// 0).  Fast path: r ~ 1/D (v_rcp_f32, 1 ulp), u = x r refined by one
-// residual step e = fma(-u, D, x), u += e r, which leaves u within 2 ulp of
-// the correctly rounded quotient (|u| <= 12 here, so 2^-19), and t = u + 8.5
-// within 2^-18 of the rule's t.  Only a t within 2^-16 of an integer can
-// truncate differently; those lanes redo the correctly rounded division.
-__device__ __forceinline__ int code_of(float x, float D, float r) {
-  float u = x * r;
-  const float e = fmaf(-u, D, x);
-  u = fmaf(e, r, u);
-  float t = u + 8.5f;
-  if (fabsf(t - __builtin_rintf(t)) < 0x1p-16f) {
-    const float ue = x / D;
-    asm volatile("" : "+v"(t));
-    t = ue + 8.5f;
-  }
-  const int q = static_cast<int>(t);  // truncation
-  return q < 0 ? 0 : (q > 15 ? 15 : q);
-}
-
 // One block: the eight lanes of a group share `blk` and hold its elements
 // 4p .. 4p + 3 in v.
 __device__ __forceinline__ void quantize_block(int64_t blk, int part, const float (&v)[4],
                                                uint8_t* __restrict__ out) {
-  // Largest magnitude inside this lane, first index on ties.
-  float best = v[0];
-  float bmag = fabsf(v[0]);
-  int bidx = part * 4;
-#pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    const float a = fabsf(v[i]);
-    if (a > bmag) { bmag = a; best = v[i]; bidx = part * 4 + i; }
-  }
-  // Across the eight lanes: both quads, then the other quad (the mirror pairs
-  // lanes whose quads already agree), so every lane ends with the same pair.
-  amax_step<kDppXor1>(best, bmag, bidx);
-  amax_step<kDppXor2>(best, bmag, bidx);
-  amax_step<kDppHalfMirror>(best, bmag, bidx);
-
-  // The quotient is exact in fp32 (a power-of-two scaling), then rounded once
-  // to fp16.  The empty asm keeps the compiler from fusing the two steps into a
-  // mixed-precision fma with a +0 addend, which would turn a -0 scale into +0
-  // (an all +0 block must get d = fp16(+0 / -8) = -0).
-  float t = best / -8.0f;
-  asm volatile("" : "+v"(t));
-  const half_t dh = static_cast<half_t>(t);
-  const float D = static_cast<float>(dh);
-
-  uint32_t nib = 0x08080808u;  // every q is 8 when d is zero
-  if (D != 0.0f) {
-    const float r = __builtin_amdgcn_rcpf(D);
-    nib = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) nib |= static_cast<uint32_t>(code_of(v[i], D, r)) << (8 * i);
-  }
-  // Lane p (< 4) holds low nibbles of code bytes 4p..4p+3; lane p+4 holds the
-  // matching high nibbles (elements 16 + 4p ..).
-  const uint32_t hi = static_cast<uint32_t>(dpp_i<kDppShl4>(static_cast<int>(nib)));
+  uint32_t bytes;
+  const half_t dh = quantize_lanes(part, v, &bytes);
   uint8_t* ob = out + blk * kBlockBytes;
   if (part < 4) {
-    const uint32_t bytes = nib | (hi << 4);
     uint16_t* dst = reinterpret_cast<uint16_t*>(ob + 2 + 4 * part);  // 2-byte aligned
     dst[0] = static_cast<uint16_t>(bytes & 0xFFFFu);
     dst[1] = static_cast<uint16_t>(bytes >> 16);

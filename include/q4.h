@@ -338,6 +338,120 @@ q4_status q4_moe(const void *x, int x_dtype, const void *logits, int logits_dtyp
                  int32_t *ids, float *weights, void *workspace, size_t workspace_bytes,
                  q4_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Cache of keys and values, and attention over it
+ * ------------------------------------------------------------------------
+ * A paged cache in Q4_0 and the attention that reads it: what stands between
+ * the q/k/v product of a decoder layer and its output product.  Conventions
+ * are those at the top of this header except where stated.
+ *
+ * The cache holds head_dim values of keys and of values for every position and
+ * kv head, quantised by the rule at the top of this header, 32 values along
+ * head_dim to a block, after these steps: a value is limited to +-65504 (an
+ * infinity counts as that, NaN as 0), so every decoded value is a finite fp16
+ * range number.  It is [pages][kv_heads][2][page_size / 16] granules of 9
+ * head_dim bytes ([2]: keys, values), sixteen positions each: 8 head_dim code
+ * bytes, then head_dim / 2 fp16 scales.  With blocks = head_dim / 32, position
+ * t = 0 .. 15 of the granule and code byte i = 0 .. 15 of a block b:
+ *   keys    code byte at t head_dim / 2 + (i / 4 blocks + b) 4 + i % 4
+ *           scale     at (t / 4 blocks + b) 4 + t % 4
+ *   values  code byte at (b 16 + i) 16 + t
+ *           scale     at b 16 + t / 4 4 + {0, 2, 1, 3}[t % 4]
+ * (integer divisions).  A byte belongs to one position alone. */
+
+#define Q4_CACHE_GRANULE 16     /* positions; page_size is a multiple of it */
+#define Q4_CACHE_MAX_HEAD_DIM 256
+#define Q4_CACHE_MAX_SEQS 65536
+
+typedef struct q4_cache {
+  void *data;         /* q4_cache_size bytes */
+  int64_t pages;      /* 1 .. 2^31 - 1 */
+  int64_t page_size;  /* positions per page: a multiple of 16, at most 2^30 */
+  int64_t kv_heads;   /* 1 .. 65535 */
+  int64_t head_dim;   /* a multiple of 32, at most Q4_CACHE_MAX_HEAD_DIM */
+} q4_cache;
+
+/* Some sequences and their rows.  Sequence s has the rows offsets[s] ..
+ * offsets[s + 1] - 1 of q, k and v, n of them, and lengths[s] positions, of
+ * which its rows are the last: its row i is position lengths[s] - n + i.
+ * Position t is in page tables[s][t / page_size].  All arrays are on the device
+ * and read when the call runs, 4-byte aligned.
+ *   - Rows before offsets[0] and from offsets[seqs] on belong to no sequence:
+ *     no call reads them or writes their outputs.
+ *   - offsets, which do not fall, are limited to 0 .. tokens, lengths to 0 ..
+ *     max_pages page_size.  A row whose position is negative has none.
+ *   - A page number outside 0 .. pages - 1 names no page: its positions are not
+ *     written, read as 0 and seen by no row.
+ *   - Positions that one call writes lie in different places (sequences may
+ *     share pages that it reads); a place that two of them name holds either's
+ *     bytes or a mixture. */
+typedef struct q4_batch {
+  int64_t seqs;           /* 1 .. Q4_CACHE_MAX_SEQS */
+  int64_t tokens;         /* rows of q, k and v, 1 .. 2^31 - 1 */
+  int64_t max_pages;      /* 1 ..; max_pages page_size is at most 2^30 */
+  const int32_t *tables;  /* [seqs][max_pages] */
+  const int32_t *lengths; /* [seqs] */
+  const int32_t *offsets; /* [seqs + 1]; NULL: row s is sequence s's only one (tokens == seqs) */
+} q4_batch;
+
+/* Bytes of a cache: pages kv_heads page_size head_dim 36 / 32 (0 for an
+ * invalid shape, or one of 2^40 values or more). */
+size_t q4_cache_size(int64_t pages, int64_t page_size, int64_t kv_heads, int64_t head_dim);
+
+/* Quantise rows of keys and values into their positions.  k and v are
+ * [tokens][kv_heads][head_dim] of `dtype`, row i at k + i k_stride and v + i
+ * v_stride elements (at least kv_heads head_dim; whole 16-byte pieces, so that
+ * rows of a fused q/k/v product are taken where they are).  Bytes of other
+ * positions are not changed. */
+q4_status q4_cache_write(const q4_cache *cache, const q4_batch *batch, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, int dtype, q4_stream_t stream);
+
+/* The decoded values (q - 8) d of the rows' positions, rounded once to `dtype`,
+ * into k and v, [tokens][kv_heads][head_dim], contiguous.  A row without a
+ * position is written as zeros. */
+q4_status q4_cache_read(const q4_cache *cache, const q4_batch *batch, void *k, void *v, int dtype,
+                        q4_stream_t stream);
+
+/* For a row at position p, head h of `heads` (a multiple of kv_heads, at most
+ * 65536; h reads kv head h / (heads / kv_heads)), over the positions t it sees:
+ *   s_t = scale q . k_t;  softcap > 0: s_t = softcap tanh(s_t / softcap)
+ *   y   = sum_t exp(s_t) v_t / sum_t exp(s_t),  lse = ln sum_t exp(s_t)
+ * It sees t < lengths[s], with `causal` t <= p, with window > 0 t > p - window.
+ * A row that sees nothing has y = 0, lse = -infinity. */
+typedef struct q4_attention_options {
+  float scale;    /* finite */
+  int causal;     /* 0 or 1 */
+  int64_t window; /* 0: none */
+  float softcap;  /* finite, >= 0; 0: none */
+} q4_attention_options;
+
+/* Bytes of workspace q4_attention needs (0 when none or for invalid arguments).
+ * `with_offsets`: whether the batch has offsets. */
+size_t q4_attention_workspace_size(int64_t seqs, int64_t tokens, int64_t heads, int64_t kv_heads,
+                                   int64_t head_dim, int q_dtype, int with_offsets);
+
+/* Softmax attention of q[tokens][heads][head_dim] (row i at q + i q_stride
+ * elements, as in q4_cache_write) over the sequences' positions in the cache,
+ * into y[tokens][heads][head_dim], contiguous, of any q4_dtype, and, unless
+ * NULL, lse[tokens][heads] (fp32).  The rows' own positions are read from the
+ * cache too: q4_cache_write comes first.
+ *   - fp32 q: fp32 products of the exactly decoded values.
+ *   - fp16 and bf16 q on matrix cores, with fp32 sums.  Sequences of few rows
+ *     (single tokens, drafts) take the keys' codes as exact integers and their
+ *     scales in fp32; sequences of many rows round the decoded keys to fp16
+ *     once.  Decoded values and the weights exp(s_t - m) are rounded to fp16
+ *     (with fp16 q and few rows the weights are kept in two fp16 parts).
+ *   - bf16 q are taken as fp16 times a power of two per row and head, as in
+ *     q4_linear.
+ * Results do not depend on what else runs, but the order of the sums over
+ * positions depends on the whole batch's lengths.  Positions that no row sees
+ * may hold anything.  `workspace` holds q4_attention_workspace_size bytes (NULL
+ * when that is 0), overlaps no other buffer and is shared by no call that may
+ * run at the same time. */
+q4_status q4_attention(const q4_cache *cache, const q4_batch *batch, const q4_attention_options *options,
+                       const void *q, int64_t q_stride, int q_dtype, int64_t heads, void *y, int y_dtype,
+                       float *lse, void *workspace, size_t workspace_bytes, q4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
