@@ -5,20 +5,13 @@
 //   y   = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),  m = max_t s_t
 //
 // in one pass over the positions that a row sees, with the running maximum and sum.
-#include "q4_cache.hpp"
+#include "q4_attention.hpp"
 
 namespace q4 {
 namespace {
 
 constexpr int kWaves = 4;
 constexpr int kMaxDim = 256;
-constexpr float kLog2e = 1.4426950408889634f;
-
-// c tanh(s / c) as c - 2 c / (exp(2 s / c) + 1): +-c where exp leaves fp32.
-__device__ __forceinline__ float capped(float s, float c) {
-  return c - 2.f * c / (expf(2.f * s / c) + 1.f);
-}
-
 // A workgroup per row and head; a wavefront takes every fourth tile of 64 positions:
 // first a position a lane (its score), then two pairs of columns a lane.  Everything
 // is fp32 on the exactly decoded values.
@@ -151,8 +144,13 @@ hipError_t launch_row(const Attention& a, Queue q) {
 
 }  // namespace
 
-size_t attention_workspace_bytes(const Attention&) { return 0; }
+size_t attention_workspace_bytes(const Attention& a) {
+  return a.qt == DType::F32 ? 0 : attention_few_bytes(a);
+}
 
-hipError_t launch_attention(const Attention& a, void*, Queue q) { return launch_row(a, q); }
+hipError_t launch_attention(const Attention& a, void* workspace, Queue q) {
+  if (a.qt == DType::F32) return launch_row(a, q);
+  return launch_attention_few(a, 1 << 30, workspace, q);
+}
 
 }  // namespace q4

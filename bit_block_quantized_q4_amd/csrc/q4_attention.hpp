@@ -1,0 +1,95 @@
+// Shared by the matrix-core kernels of the attention over the paged Q4_0 cache
+// (gfx950).  Internal header.
+//
+// Scores are kept in units of log2: x = s log2 e, weights exp2(x - m).  A weight is
+// held times 2^12 (kLift): fp16 then keeps its full 11 bits down to 2^-26 of the
+// largest, and a single weight of 2^12 stays far below fp16's range.
+#pragma once
+
+#include "q4_cache.hpp"
+
+namespace q4 {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLift = 12.f;
+
+// c tanh(s / c) as c - 2 c / (exp(2 s / c) + 1): +-c where exp leaves fp32.
+__device__ __forceinline__ float capped(float s, float c) {
+  return c - 2.f * c / (exp2f(2.f * kLog2e * s / c) + 1.f);
+}
+
+// The same from s and back in units of log2, for many scores: as c - 2 c / (e + 1) with
+// the reciprocal of the hardware (1 ulp).
+struct Cap {
+  float c, in, out;
+  __device__ __forceinline__ explicit Cap(float cap) : c(cap * kLog2e), in(2.f * kLog2e / cap), out(-2.f * cap * kLog2e) {}
+  __device__ __forceinline__ float of(float s) const {
+    const float e = __builtin_amdgcn_exp2f(s * in);
+    return fmaf(out, __builtin_amdgcn_rcpf(e + 1.f), c);
+  }
+};
+
+// The larger / the sum of the values that the lanes of the same l % 16 hold.
+__device__ __forceinline__ float max_over_groups(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  v = fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(p[0])), __builtin_bit_cast(float, static_cast<uint32_t>(p[1])));
+  const uint32_t c = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+  return fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
+}
+__device__ __forceinline__ float sum_over_groups(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  v = __builtin_bit_cast(float, static_cast<uint32_t>(p[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(p[1]));
+  const uint32_t c = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+  return __builtin_bit_cast(float, static_cast<uint32_t>(r[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(r[1]));
+}
+
+// The exact q - 8 of a dword's eight codes, as fp16 pairs of bytes (0, 2) and (1, 3):
+// low nibbles l02, l13, high nibbles h02, h13.  (A nibble in the low bits of a fixed
+// exponent is 1024 + q or 64 + q.)
+struct Codes {
+  half2_t l02, l13, h02, h13;
+};
+__device__ __forceinline__ Codes codes_of(uint32_t w, const UnpackConsts& k) {
+  const uint32_t v = w >> 8;
+  const half2_t klo = {static_cast<half_t>(-1032.0f), static_cast<half_t>(-1032.0f)};
+  const half2_t khi = {static_cast<half_t>(-72.0f), static_cast<half_t>(-72.0f)};
+  Codes c;
+  c.l02 = __builtin_bit_cast(half2_t, (w & k.mask_lo) | k.exp_lo) + klo;
+  c.l13 = __builtin_bit_cast(half2_t, (v & k.mask_lo) | k.exp_lo) + klo;
+  c.h02 = __builtin_bit_cast(half2_t, (w & k.mask_hi) | k.exp_hi) + khi;
+  c.h13 = __builtin_bit_cast(half2_t, (v & k.mask_hi) | k.exp_hi) + khi;
+  return c;
+}
+
+__device__ __forceinline__ half8_t join(half2_t a, half2_t b, half2_t c, half2_t d) {
+  u32x4 r;
+  r[0] = __builtin_bit_cast(uint32_t, a);
+  r[1] = __builtin_bit_cast(uint32_t, b);
+  r[2] = __builtin_bit_cast(uint32_t, c);
+  r[3] = __builtin_bit_cast(uint32_t, d);
+  return __builtin_bit_cast(half8_t, r);
+}
+
+// Four consecutive outputs from column `at` on (a multiple of four).
+__device__ __forceinline__ void store4(void* y, int dt, int64_t at, const float (&v)[4]) {
+  if (dt == static_cast<int>(DType::F32)) {
+    float4_t r = {v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<float4_t*>(static_cast<float*>(y) + at) = r;
+  } else {
+    uint2 r;
+    r.x = f32_to_16(v[0], dt) | static_cast<uint32_t>(f32_to_16(v[1], dt)) << 16;
+    r.y = f32_to_16(v[2], dt) | static_cast<uint32_t>(f32_to_16(v[3], dt)) << 16;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = r;
+  }
+}
+
+// Sequences of at most max_rows rows (query rows times heads per kv head).
+size_t attention_few_bytes(const Attention& a);
+hipError_t launch_attention_few(const Attention& a, int max_rows, void* workspace, Queue q);
+
+}  // namespace q4
