@@ -358,7 +358,8 @@ def _fast():
             _q4_torch.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
                 "q4_linear", "q4_linear_workspace_size", "q4_route", "q4_route_plan",
                 "q4_route_plan_size", "q4_experts", "q4_experts_workspace_size", "q4_moe",
-                "q4_moe_workspace_size")))
+                "q4_moe_workspace_size", "q4_cache_write", "q4_cache_read", "q4_attention",
+                "q4_attention_workspace_size")))
             _FAST = _q4_torch
     return _FAST or None
 
@@ -842,6 +843,9 @@ def q4_cache_write(k, v, cache, tables, lengths, offsets=None, stream=None):
     if stream is not None:
         with _on(stream, k):
             return q4_cache_write(k, v, cache, tables, lengths, offsets)
+    fast = _FAST or _fast()
+    if fast is not None and fast.cache_write(k, v, cache, tables, lengths, offsets):
+        return
     index = _same_device_rows(k, {"v": v}, cache=cache, tables=tables, lengths=lengths, offsets=offsets)
     c = _cache_arg(cache)
     ks, vs = _row_stride(k, "k", c.kv_heads, c.head_dim), _row_stride(v, "v", c.kv_heads, c.head_dim)
@@ -863,6 +867,14 @@ def q4_cache_read(cache, tables, lengths, offsets=None, tokens=None, dtype=None,
         with _on(stream, cache):
             return q4_cache_read(cache, tables, lengths, offsets, tokens, dtype, k, v)
     torch = _torch()
+    if k is None and v is None:
+        fast = _FAST or _fast()
+        if fast is not None:
+            code = 1 if dtype is None or dtype is torch.float16 else 2 if dtype is torch.bfloat16 else (
+                0 if dtype is torch.float32 else -1)
+            out = fast.cache_read(cache, tables, lengths, offsets, -1 if tokens is None else tokens, code)
+            if out is not None:
+                return out
     index = _same_device_rows(cache, {}, cache=cache, tables=tables, lengths=lengths, offsets=offsets, k=k, v=v)
     c = _cache_arg(cache)
     if tokens is None:
@@ -909,6 +921,12 @@ def q4_attention(q, cache, tables, lengths, offsets=None, scale=None, causal=Tru
         with _on(stream, q):
             return q4_attention(q, cache, tables, lengths, offsets, scale, causal, window, softcap, return_lse, y,
                                 y_dtype, lse, workspace)
+    if y is None and y_dtype is None and lse is None and workspace is None:
+        fast = _FAST or _fast()
+        if fast is not None:
+            out = fast.attention(q, cache, tables, lengths, offsets, scale, causal, window, softcap, return_lse)
+            if out is not None:
+                return out
     torch = _torch()
     index = _same_device_rows(q, {}, cache=cache, tables=tables, lengths=lengths, offsets=offsets, y=y, lse=lse,
                               workspace=workspace)

@@ -1,4 +1,4 @@
-// Short way from Python to libq4's fused calls, for small layers, where the
+// Short way from Python to libq4's fused calls and its cache, for small layers, where the
 // time of a call is the time of its Python (7 of 11 us for a 512 x 512 row).
 //
 // Each function takes the Python function's arguments by position, checks that
@@ -16,6 +16,8 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
+
 #include "q4.h"
 
 namespace {
@@ -29,6 +31,10 @@ decltype(&q4_experts) p_experts;
 decltype(&q4_experts_workspace_size) p_experts_ws;
 decltype(&q4_moe) p_moe;
 decltype(&q4_moe_workspace_size) p_moe_ws;
+decltype(&q4_cache_write) p_cache_write;
+decltype(&q4_cache_read) p_cache_read;
+decltype(&q4_attention) p_attention;
+decltype(&q4_attention_workspace_size) p_attention_ws;
 
 // The arguments of one call: the first tensor names the device, and every check
 // that fails is remembered.
@@ -38,8 +44,9 @@ struct Call {
   bool ok = true;
   int device = -1;
 
-  // Argument i as a tensor of the call's device, or nullptr for None.
-  const at::Tensor* tensor(int i) {
+  // Argument i as a tensor of the call's device, or nullptr for None.  strided: one
+  // that need not be contiguous.
+  const at::Tensor* tensor(int i, bool strided = false) {
     PyObject* o = args[i];
     if (o == Py_None) return nullptr;
     if (!THPVariable_Check(o)) {
@@ -47,7 +54,7 @@ struct Call {
       return nullptr;
     }
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || !t.is_contiguous() || (grad && t.requires_grad()) || t._fw_grad(0).defined()) {
+    if (!t.is_cuda() || (!strided && !t.is_contiguous()) || (grad && t.requires_grad()) || t._fw_grad(0).defined()) {
       ok = false;
       return nullptr;
     }
@@ -56,8 +63,8 @@ struct Call {
     if (d != device) ok = false;
     return &t;
   }
-  const at::Tensor* needed(int i) {
-    const at::Tensor* t = tensor(i);
+  const at::Tensor* needed(int i, bool strided = false) {
+    const at::Tensor* t = tensor(i, strided);
     if (t == nullptr) ok = false;
     return t;
   }
@@ -287,14 +294,128 @@ PyObject* moe(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// A cache [pages, kv heads, 2, page size / 16, 9 d] and a batch over it, from args[at]:
+// cache, tables, lengths, offsets (or None).
+struct CacheCall {
+  q4_cache cache;
+  q4_batch batch;
+  const at::Tensor* data;
+  bool take(Call& c, int at, int64_t tokens) {
+    data = c.needed(at);
+    const at::Tensor *tables = c.needed(at + 1), *lengths = c.needed(at + 2), *offsets = c.tensor(at + 3);
+    if (!c.ok) return false;
+    c.want(data->dim() == 5 && data->scalar_type() == at::kByte && tables->dim() == 2 && lengths->dim() == 1);
+    if (!c.ok) return false;
+    c.want(data->size(2) == 2 && data->size(4) % (9 * Q4_QK) == 0 && tables->scalar_type() == at::kInt &&
+           lengths->scalar_type() == at::kInt && lengths->size(0) == tables->size(0));
+    const int64_t seqs = tables->size(0);
+    c.want(offsets ? offsets->dim() == 1 && offsets->scalar_type() == at::kInt && offsets->size(0) == seqs + 1
+                   : tokens < 0 || tokens == seqs);
+    if (!c.ok) return false;
+    cache = q4_cache{const_cast<void*>(data->const_data_ptr()), data->size(0), data->size(3) * Q4_CACHE_GRANULE,
+                     data->size(1), data->size(4) / 9};
+    batch = q4_batch{seqs, tokens < 0 ? seqs : tokens, tables->size(1),
+                     static_cast<const int32_t*>(tables->const_data_ptr()),
+                     static_cast<const int32_t*>(lengths->const_data_ptr()),
+                     offsets ? static_cast<const int32_t*>(offsets->const_data_ptr()) : nullptr};
+    return true;
+  }
+  // Elements between the rows of t [tokens, heads, d], whose heads lie together.
+  int64_t stride(Call& c, const at::Tensor& t) {
+    const int64_t width = t.size(1) * cache.head_dim;
+    c.want(t.size(2) == cache.head_dim && t.stride(2) == 1 && (t.size(1) == 1 || t.stride(1) == cache.head_dim));
+    return t.size(0) > 1 || t.stride(0) >= width ? t.stride(0) : width;
+  }
+};
+
+// k, v, then a cache call -> True
+PyObject* cache_write(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 6) return nullptr;
+    Call c{args};
+    const at::Tensor *k = c.needed(0, true), *v = c.needed(1, true);
+    if (!c.ok || k->dim() != 3 || v->sizes() != k->sizes() || v->scalar_type() != k->scalar_type()) return nullptr;
+    CacheCall cc;
+    if (!cc.take(c, 2, k->size(0))) return nullptr;
+    c.want(k->size(1) == cc.cache.kv_heads);
+    const int64_t ks = cc.stride(c, *k), vs = cc.stride(c, *v);
+    const int dt = c.dtype(*k);
+    cc.cache.data = cc.data->mutable_data_ptr();
+    if (!c.ready() || p_cache_write(&cc.cache, &cc.batch, k->const_data_ptr(), ks, v->const_data_ptr(), vs, dt,
+                                    c.stream()) != Q4_OK)
+      return nullptr;
+    Py_RETURN_TRUE;
+  });
+}
+
+// A cache call, tokens (-1: one a sequence), dtype (0, 1, 2 as in q4_dtype) -> (k, v)
+PyObject* cache_read(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 6) return nullptr;
+    Call c{args};
+    const int64_t tokens = PyLong_Check(args[4]) ? PyLong_AsLongLong(args[4]) : 0, dt = c.integer(5);
+    c.want(tokens >= 1 || (tokens == -1 && args[3] == Py_None));
+    CacheCall cc;
+    if (!c.ok || dt < 0 || dt > 2 || !cc.take(c, 0, tokens) || !c.ready()) return nullptr;
+    const auto options =
+        cc.data->options().dtype(dt == Q4_F32 ? at::kFloat : dt == Q4_F16 ? at::kHalf : at::kBFloat16);
+    at::Tensor k = at::empty({cc.batch.tokens, cc.cache.kv_heads, cc.cache.head_dim}, options), v = at::empty_like(k);
+    if (p_cache_read(&cc.cache, &cc.batch, k.mutable_data_ptr(), v.mutable_data_ptr(), static_cast<int>(dt),
+                     c.stream()) != Q4_OK)
+      return nullptr;
+    PyObject* t = PyTuple_New(2);
+    if (t == nullptr) return nullptr;
+    PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(k));
+    PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(v));
+    return t;
+  });
+}
+
+// q, then a cache call, scale (or None), causal, window, softcap, whether lse is asked -> y or (y, lse)
+PyObject* attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 10) return nullptr;
+    Call c{args};
+    const at::Tensor* q = c.needed(0, true);
+    if (!c.ok || q->dim() != 3) return nullptr;
+    CacheCall cc;
+    if (!cc.take(c, 1, q->size(0))) return nullptr;
+    const int64_t qs = cc.stride(c, *q), window = c.integer(7), heads = q->size(1), tokens = q->size(0);
+    const bool causal = c.truth(6), with_lse = c.truth(9);
+    c.want((args[5] == Py_None || PyFloat_Check(args[5])) && PyFloat_Check(args[8]));
+    const int qd = c.dtype(*q);
+    if (!c.ready()) return nullptr;
+    const q4_attention_options options{
+        static_cast<float>(args[5] == Py_None ? 1.0 / std::sqrt(static_cast<double>(cc.cache.head_dim))
+                                              : PyFloat_AS_DOUBLE(args[5])),
+        causal ? 1 : 0, window, static_cast<float>(PyFloat_AS_DOUBLE(args[8]))};
+    at::Tensor y = at::empty({tokens, heads, cc.cache.head_dim}, q->options()), lse, ws;
+    if (with_lse) lse = at::empty({tokens, heads}, q->options().dtype(at::kFloat));
+    const size_t need = p_attention_ws(cc.batch.seqs, tokens, heads, cc.cache.kv_heads, cc.cache.head_dim, qd,
+                                       cc.batch.offsets != nullptr);
+    if (need > 0) ws = bytes(y, need);
+    if (p_attention(&cc.cache, &cc.batch, &options, q->const_data_ptr(), qs, qd, heads, y.mutable_data_ptr(), qd,
+                    with_lse ? static_cast<float*>(lse.mutable_data_ptr()) : nullptr,
+                    need > 0 ? ws.mutable_data_ptr() : nullptr, need, c.stream()) != Q4_OK)
+      return nullptr;
+    if (!with_lse) return THPVariable_Wrap(y);
+    PyObject* t = PyTuple_New(2);
+    if (t == nullptr) return nullptr;
+    PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(y));
+    PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(lse));
+    return t;
+  });
+}
+
 // Addresses of the library's entry points, in this order.
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  void* p[9];
-  if (n != 9) {
-    PyErr_SetString(PyExc_TypeError, "bind takes nine addresses");
+  constexpr int kAddresses = 13;
+  void* p[kAddresses];
+  if (n != kAddresses) {
+    PyErr_SetString(PyExc_TypeError, "bind takes thirteen addresses");
     return nullptr;
   }
-  for (int i = 0; i < 9; ++i) {
+  for (int i = 0; i < kAddresses; ++i) {
     p[i] = PyLong_AsVoidPtr(args[i]);
     if (p[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: null address");
@@ -310,12 +431,17 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   p_experts_ws = reinterpret_cast<decltype(p_experts_ws)>(p[6]);
   p_moe = reinterpret_cast<decltype(p_moe)>(p[7]);
   p_moe_ws = reinterpret_cast<decltype(p_moe_ws)>(p[8]);
+  p_cache_write = reinterpret_cast<decltype(p_cache_write)>(p[9]);
+  p_cache_read = reinterpret_cast<decltype(p_cache_read)>(p[10]);
+  p_attention = reinterpret_cast<decltype(p_attention)>(p[11]);
+  p_attention_ws = reinterpret_cast<decltype(p_attention_ws)>(p[12]);
   Py_RETURN_NONE;
 }
 
 #define Q4_FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {Q4_FAST(bind), Q4_FAST(linear), Q4_FAST(route), Q4_FAST(route_plan),
-                         Q4_FAST(experts), Q4_FAST(moe), {nullptr, nullptr, 0, nullptr}};
+                         Q4_FAST(experts), Q4_FAST(moe), Q4_FAST(cache_write),
+                         Q4_FAST(cache_read), Q4_FAST(attention), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_q4_torch", nullptr, -1, methods};
 
 }  // namespace

@@ -48,6 +48,18 @@ __device__ __forceinline__ float sum_over_groups(float v) {
   return __builtin_bit_cast(float, static_cast<uint32_t>(r[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(r[1]));
 }
 
+// As those, over the lanes l and l + 32.
+__device__ __forceinline__ float max_over_halves(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(p[0])), __builtin_bit_cast(float, static_cast<uint32_t>(p[1])));
+}
+__device__ __forceinline__ float sum_over_halves(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __builtin_bit_cast(float, static_cast<uint32_t>(p[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(p[1]));
+}
+
 // The exact q - 8 of a dword's eight codes, as fp16 pairs of bytes (0, 2) and (1, 3):
 // low nibbles l02, l13, high nibbles h02, h13.  (A nibble in the low bits of a fixed
 // exponent is 1024 + q or 64 + q.)
@@ -91,5 +103,10 @@ __device__ __forceinline__ void store4(void* y, int dt, int64_t at, const float 
 // Sequences of at most max_rows rows (query rows times heads per kv head).
 size_t attention_few_bytes(const Attention& a);
 hipError_t launch_attention_few(const Attention& a, int max_rows, void* workspace, Queue q);
+
+
+// Sequences of at least min_rows.
+size_t attention_many_bytes(const Attention& a);
+hipError_t launch_attention_many(const Attention& a, int min_rows, void* workspace, Queue q);
 
 }  // namespace q4

@@ -1,0 +1,486 @@
+// Attention over the paged Q4_0 cache for sequences of many rows: prompts and chunks
+// of them.
+//
+//   S^T = K Q^T,  P = exp2(x - m),  O^T = V^T P^T
+//
+// with keys and values rounded to fp16 as they are decoded, once for all the rows of a
+// workgroup.  A kv head's heads and a sequence's rows together are the rows; a
+// wavefront takes 32 of them, a workgroup as many as it has wavefronts, and walks over
+// the positions in tiles of 64.  Each tile is decoded into one of two LDS buffers by
+// all wavefronts (wavefront w the granule w % 4) while the other is multiplied; the
+// next tile's bytes are on their way in registers meanwhile.
+//
+// LDS holds 16-byte pieces, the operands of v_mfma_f32_32x32x16_f16 as they are read:
+//   K  position t, piece 4 b + g: elements 4 g + {0, 2, 1, 3, 16, 18, 17, 19} of block
+//      b (the order in which a code word comes apart; q is held in the same order)
+//   V  column c, piece 2 k + h: positions 16 k + 4 h + {0, 2, 1, 3, 8, 10, 9, 11}, which
+//      is what lane half h holds of the scores' rows: the weights are the right operand
+//      of the second product where they are
+// The piece number is exclusive-ored with the row's so that rows lie in other banks.
+//
+// Where there are fewer workgroups than compute units the positions are split as well,
+// and the parts joined in a second launch.
+#include "q4_attention.hpp"
+
+namespace q4 {
+namespace {
+
+constexpr int kTile = 64;
+constexpr float kLift2 = 8.f;   // weights are held times 2^8 ..
+constexpr float kSlack = 7.f;   // .. of a maximum that may have grown by 2^7 since
+
+struct Many {
+  int min_rows = 0;   // sequences of fewer rows are left out
+  int splits = 1;
+  float* stats = nullptr;   // [workgroups][rows][2]
+  float4_t* cols = nullptr; // [workgroups][wavefronts][NB][4][64]
+};
+
+// Row tiles of R rows, as places of a grid: sequence s has the places from
+// row_place(s) on, more than it has tiles.
+__device__ __forceinline__ int64_t row_place(const Batch& b, int group, int rows, int s) {
+  return static_cast<int64_t>(offset_of(b, s)) * group / rows + s;
+}
+
+// What workgroup `at` takes: heads inside (neighbours, which lie on other dies, then
+// read other keys), the last rows, which see most, first.
+template <int R>
+__device__ __forceinline__ bool job_of(const Attention& a, const Many& y, int64_t at, int64_t places, int* s, int* h,
+                                       int* r0, int* rows, int* split, Seq* q) {
+  const int kv = a.cache.kv_heads;
+  *h = static_cast<int>(at % kv);
+  at /= kv;
+  *split = static_cast<int>(at % y.splits);
+  const int64_t place = places - 1 - at / y.splits;
+  *s = a.batch.offsets == nullptr ? static_cast<int>(place) : last_not_above(a.batch.seqs, place, [&](int i) {
+    return row_place(a.batch, a.group, R, i);
+  });
+  *q = seq_of(a.batch, *s);
+  const int64_t n = static_cast<int64_t>(q->rows) * a.group;
+  const int64_t first = a.batch.offsets == nullptr ? 0 : (place - row_place(a.batch, a.group, R, *s)) * R;
+  if (n < y.min_rows || first < 0 || first >= n) return false;
+  *r0 = static_cast<int>(first);
+  *rows = static_cast<int>(n);
+  return true;
+}
+
+template <int NB>
+struct Bytes {
+  uint32_t k[NB];
+  uint16_t ks[NB];
+  u32x4 v[(NB + 3) / 4], vs[(NB + 3) / 4][2];
+};
+
+template <int NB, int WAVES, bool BF16>
+__global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel(Attention a, Many y, int64_t places) {
+  constexpr int R = 32 * WAVES;
+  constexpr int kPieces = 4 * NB;                 // of a position's key
+  constexpr int kSwizzle = NB % 4 == 0 ? 15 : NB % 2 == 0 ? 7 : 3;  // 4 NB is a multiple of one more
+  constexpr int kKeys = kTile * kPieces, kValues = NB * kQK * 8;
+  extern __shared__ __attribute__((aligned(16))) uint8_t dynamic[];
+  // [2] buffers of keys and values, then [2][4] whether a granule has a page
+  u32x4* const lds = reinterpret_cast<u32x4*>(dynamic);
+  int* const named = reinterpret_cast<int*>(dynamic + 2 * (kKeys + kValues) * 16);
+
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n = lane & 31, half = lane >> 5;
+  int s, h, r0, rows, split;
+  Seq q;
+  if (!job_of<R>(a, y, blockIdx.x, places, &s, &h, &r0, &rows, &split, &q)) return;
+  const Cache& c = a.cache;
+  const UnpackConsts uc = make_unpack_consts();
+  const Cap cap(a.softcap);
+
+  // The tiles of all the workgroup's rows, and of this part of them.
+  const int end_row = r0 + R < rows ? r0 + R : rows;
+  int lo_first, hi_first, lo_last, hi_last;
+  seen_by(a, q.length, q.first + r0 / a.group, &lo_first, &hi_first);
+  seen_by(a, q.length, q.first + (end_row - 1) / a.group, &lo_last, &hi_last);
+  const int tile0 = lo_first / kTile, tiles = hi_last > lo_first ? (hi_last + kTile - 1) / kTile - tile0 : 0;
+  const int t0 = tile0 + static_cast<int>(static_cast<int64_t>(tiles) * split / y.splits);
+  const int t1 = tile0 + static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / y.splits);
+
+  // This wavefront's rows, and what this lane's row sees.
+  const int w0 = r0 + 32 * wave, w1 = w0 + 32 < end_row ? w0 + 32 : end_row;
+  int wlo = 0, whi = 0, wlo_last = 0, whi_first = 0;
+  if (w0 < w1) {
+    seen_by(a, q.length, q.first + w0 / a.group, &wlo, &whi_first);
+    seen_by(a, q.length, q.first + (w1 - 1) / a.group, &wlo_last, &whi);
+  }
+  const int row = w0 + n < end_row ? w0 + n : end_row - 1;
+  const int token = row / a.group, hq = h * a.group + row - token * a.group;
+  int lo, hi;
+  seen_by(a, q.length, q.first + token, &lo, &hi);
+  if (w0 + n >= end_row) lo = hi = 0;
+
+  // q as the right operand: pieces 4 b + g for g = half, half + 2.
+  half8_t qf[2 * NB];
+  float mul = fabsf(a.scale) * (a.softcap > 0.f ? 1.f : kLog2e);
+  {
+    const uint16_t* x = static_cast<const uint16_t*>(a.q) + (q.row + token) * a.q_stride +
+                        static_cast<int64_t>(hq) * (NB * kQK) + 4 * half;
+    uint2 part[2 * NB][2];
+#pragma unroll
+    for (int i = 0; i < 2 * NB; ++i) {
+      part[i][0] = *reinterpret_cast<const uint2*>(x + i / 2 * kQK + 8 * (i % 2));
+      part[i][1] = *reinterpret_cast<const uint2*>(x + i / 2 * kQK + 8 * (i % 2) + 16);
+    }
+    if constexpr (BF16) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top = max_magnitude_bf16(top, part[i][e].x);
+          top = max_magnitude_bf16(top, part[i][e].y);
+        }
+      top = __builtin_bit_cast(uint32_t, max_over_halves(__builtin_bit_cast(float, top << 16))) >> 16;
+      const int shift = bf16_row_shift(top);
+      const float by = power_of_two(shift);
+      mul *= power_of_two(-shift);
+#pragma unroll
+      for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          part[i][e].x = bf16x2_scaled_to_f16x2(part[i][e].x, by);
+          part[i][e].y = bf16x2_scaled_to_f16x2(part[i][e].y, by);
+        }
+    }
+    // The factor is positive, so that the largest score is the largest product's: a
+    // negative scale turns q, one of 0 clears it.
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u, keep = a.scale == 0.f ? 0u : ~0u;
+    mul = fmaxf(mul, 1.17549435e-38f);
+#pragma unroll
+    for (int i = 0; i < 2 * NB; ++i) {
+      u32x4 v;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        v[2 * e] = __builtin_amdgcn_perm(part[i][e].y, part[i][e].x, 0x05040100) & keep ^ flip;
+        v[2 * e + 1] = __builtin_amdgcn_perm(part[i][e].y, part[i][e].x, 0x07060302) & keep ^ flip;
+      }
+      qf[i] = __builtin_bit_cast(half8_t, v);
+    }
+  }
+
+  // Fetching and decoding: wavefront w has granule w % 4 of a tile, the keys in the
+  // first four wavefronts, the values in the last four (of four: both).
+  const bool keys_here = wave < 4, values_here = WAVES == 4 || wave >= 4;
+  const int mine = wave & 3;
+  const int* table = a.batch.tables + static_cast<int64_t>(s) * a.batch.max_pages;
+  const int64_t to_values = static_cast<int64_t>(c.per_page) * (288 * NB);
+  Bytes<NB> bytes;
+  int fetched_named = 0;
+  auto fetch = [&](int tile) {
+    const uint32_t gi = static_cast<uint32_t>(tile * 4 + mine), per = static_cast<uint32_t>(c.per_page);
+    uint32_t slot = __umulhi(gi, c.inverse), in = gi - slot * per;
+    if (in >= per) {
+      ++slot;
+      in -= per;
+    }
+    const int id = slot < static_cast<uint32_t>(a.batch.max_pages) ? table[slot] : -1;
+    fetched_named = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.pages);
+    const uint8_t* p = c.data + (fetched_named ? id : 0) * c.page_bytes + h * c.head_bytes +
+                       static_cast<int64_t>(in) * (288 * NB);
+    if (keys_here) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(p) + lane * NB;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) bytes.k[b] = w[b];
+      const uint16_t* sc = reinterpret_cast<const uint16_t*>(p + 256 * NB) + (lane >> 4) * (4 * NB) + ((lane >> 2) & 3);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) bytes.ks[b] = sc[4 * b];
+    }
+    if (values_here) {
+      p += to_values;
+#pragma unroll
+      for (int i = 0; i < (NB + 3) / 4; ++i) {
+        const int at = 64 * i + lane;  // block at / 16, byte at % 16
+        if (64 * i + 64 <= 16 * NB || at < 16 * NB) {
+          bytes.v[i] = *reinterpret_cast<const u32x4*>(p + at * 16);
+          bytes.vs[i][0] = *reinterpret_cast<const u32x4*>(p + 256 * NB + at / 16 * 32);
+          bytes.vs[i][1] = *reinterpret_cast<const u32x4*>(p + 256 * NB + at / 16 * 32 + 16);
+        }
+      }
+    }
+  };
+  auto decode = [&](int tile, int buffer) {
+    u32x4* const keys = lds + buffer * (kKeys + kValues);
+    u32x4* const values = keys + kKeys;
+    if (keys_here) {
+      const int t = 16 * mine + (lane >> 2), g = lane & 3;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const Codes k = codes_of(bytes.k[b], uc);
+        const half_t d = __builtin_bit_cast(half_t, bytes.ks[b]);
+        const half2_t dd = {d, d};
+        const half8_t piece = join(k.l02 * dd, k.l13 * dd, k.h02 * dd, k.h13 * dd);
+        keys[t * kPieces + ((4 * b + g) ^ (t & kSwizzle))] = __builtin_bit_cast(u32x4, piece);
+      }
+      if (lane == 0) named[buffer * 4 + mine] = fetched_named;
+    }
+    if (values_here) {
+      const int first = tile * kTile + 16 * mine;
+      const int from = lo_first - first, to = fetched_named ? hi_last - first : 0;
+      const bool whole = from <= 0 && to >= 16;  // unseen places may hold anything
+#pragma unroll
+      for (int i = 0; i < (NB + 3) / 4; ++i) {
+        const int at = 64 * i + lane;
+        if (64 * i + 64 > 16 * NB && at >= 16 * NB) break;
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int p = e / 2 * 4 + e % 2;
+            const uint32_t keep = (p >= from && p < to ? 0xFFFFu : 0u) |
+                                  (p + 2 >= from && p + 2 < to ? 0xFFFF0000u : 0u);
+            bytes.vs[i][e >> 2][e & 3] &= keep;
+          }
+        }
+        const int col = at / 16 * 32 + at % 16;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const Codes v0 = codes_of(bytes.v[i][hf], uc), v1 = codes_of(bytes.v[i][hf + 2], uc);
+          const half2_t d0 = __builtin_bit_cast(half2_t, static_cast<uint32_t>(bytes.vs[i][0][2 * hf]));
+          const half2_t d1 = __builtin_bit_cast(half2_t, static_cast<uint32_t>(bytes.vs[i][0][2 * hf + 1]));
+          const half2_t d2 = __builtin_bit_cast(half2_t, static_cast<uint32_t>(bytes.vs[i][1][2 * hf]));
+          const half2_t d3 = __builtin_bit_cast(half2_t, static_cast<uint32_t>(bytes.vs[i][1][2 * hf + 1]));
+          const half8_t low = join(v0.l02 * d0, v0.l13 * d1, v1.l02 * d2, v1.l13 * d3);
+          const half8_t high = join(v0.h02 * d0, v0.h13 * d1, v1.h02 * d2, v1.h13 * d3);
+          values[col * 8 + ((2 * mine + hf) ^ (col & 7))] = __builtin_bit_cast(u32x4, low);
+          values[(col + 16) * 8 + ((2 * mine + hf) ^ (col & 7))] = __builtin_bit_cast(u32x4, high);
+        }
+      }
+    }
+  };
+
+  float m = -INFINITY, l = 0.f;  // m: what weights are taken against, at most kSlack below the maximum
+  float16_t o[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
+
+  if (t0 < t1) {
+    fetch(t0);
+    decode(t0, 0);
+    if (t0 + 1 < t1) fetch(t0 + 1);
+    __syncthreads();
+  }
+  for (int t = t0; t < t1; ++t) {
+    const int buffer = (t - t0) & 1, first = t * kTile;
+    const bool seen = w0 < w1 && first < whi && first + kTile > wlo;
+    const u32x4* const keys = lds + buffer * (kKeys + kValues);
+    const u32x4* const values = keys + kKeys;
+    half8_t p[4];
+    if (seen) {
+      float16_t x[2];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[mt][i] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 2 * NB; ++ks) {
+          const half8_t kf = __builtin_bit_cast(
+              half8_t, keys[(32 * mt + n) * kPieces + ((2 * ks + half) ^ (n & kSwizzle))]);
+          x[mt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[ks], x[mt], 0, 0, 0);
+        }
+      }
+      const int4 nm = *reinterpret_cast<const int4*>(named + 4 * buffer);
+      const bool all = (nm.x & nm.y & nm.z & nm.w) != 0;
+      float by = mul;
+      if (a.softcap > 0.f) {
+        by = 1.f;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[mt][i] = cap.of(x[mt][i] * mul);
+      }
+      if (!(first >= wlo_last && first + kTile <= whi_first && all && w1 == w0 + 32)) {
+        const int from = lo - first - 4 * half, to = hi - first - 4 * half;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int e = 32 * mt + 8 * (i / 4) + i % 4;
+            const int there = e / 16 == 0 ? nm.x : e / 16 == 1 ? nm.y : e / 16 == 2 ? nm.z : nm.w;
+            x[mt][i] = there && e >= from && e < to ? x[mt][i] : -INFINITY;
+          }
+      }
+      float top = fmaxf(x[0][0], x[1][0]);
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(x[0][i], x[1][i]), top);
+      top = max_over_halves(top) * by;
+      if (__any(top > m + kSlack)) {
+        const float next = fmaxf(m, top);
+        const float old = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - next);
+        m = next;
+        l *= old;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[b][i] *= old;
+      }
+      const float from = kLift2 - (m == -INFINITY ? 0.f : m);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          x[mt][i] = __builtin_amdgcn_exp2f(fmaf(x[mt][i], by, from));
+          l += x[mt][i];
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          constexpr int kOrder[8] = {0, 2, 1, 3, 4, 6, 5, 7};
+          half_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = static_cast<half_t>(x[mt][8 * ks + kOrder[e]]);
+          p[2 * mt + ks] = half8_t{w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+        }
+      }
+    }
+    if (t + 1 < t1) {
+      decode(t + 1, buffer ^ 1);
+      if (t + 2 < t1) fetch(t + 2);
+    }
+    if (seen) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const half8_t vf = __builtin_bit_cast(half8_t, values[(32 * b + n) * 8 + ((2 * k + half) ^ (n & 7))]);
+          o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[k], o[b], 0, 0, 0);
+        }
+    }
+    __syncthreads();
+  }
+
+  l = sum_over_halves(l);
+  if (y.splits > 1) {
+    const int64_t at = (blockIdx.x * static_cast<int64_t>(WAVES) + wave);
+    if (half == 0) *reinterpret_cast<float2*>(y.stats + (at * 32 + n) * 2) = float2{m, l};
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        y.cols[((at * NB + b) * 4 + i) * kWave + lane] =
+            float4_t{o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]};
+    return;
+  }
+  if (w0 + n >= end_row) return;
+  const int64_t at = static_cast<int64_t>(q.row + token) * a.heads + hq;
+  const float inverse = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float out[4] = {o[b][4 * i] * inverse, o[b][4 * i + 1] * inverse, o[b][4 * i + 2] * inverse,
+                            o[b][4 * i + 3] * inverse};
+      store4(a.y, a.y_dt, at * (NB * kQK) + b * kQK + 8 * i + 4 * half, out);
+    }
+  if (a.lse != nullptr && half == 0) a.lse[at] = l > 0.f ? (m - kLift2 + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// The splits' parts of a row tile, in their order; a wavefront takes 32 rows of 32 columns.
+template <int NB, int WAVES>
+__global__ __launch_bounds__(kWave) void attention_splits_kernel(Attention a, Many y, int64_t places) {
+  constexpr int R = 32 * WAVES;
+  const int lane = threadIdx.x, n = lane & 31, half = lane >> 5;
+  const int wave = blockIdx.y / NB, b = blockIdx.y % NB;
+  const int kv = a.cache.kv_heads;
+  const int64_t place = blockIdx.x / kv;  // as the first launch counts them, without its splits
+  const int64_t block0 = place * y.splits * kv + blockIdx.x % kv;
+  int s, h, r0, rows, split;
+  Seq q;
+  if (!job_of<R>(a, y, block0, places, &s, &h, &r0, &rows, &split, &q)) return;
+  const int row = r0 + 32 * wave + n;
+  float m = -INFINITY, l = 0.f;
+  float4_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = float4_t{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < y.splits; ++i) {
+    const int64_t at = (block0 + static_cast<int64_t>(i) * kv) * WAVES + wave;
+    const float2 st = *reinterpret_cast<const float2*>(y.stats + (at * 32 + n) * 2);
+    const float next = fmaxf(m, st.x), ref = next == -INFINITY ? 0.f : next;
+    const float old = __builtin_amdgcn_exp2f(m - ref), by = __builtin_amdgcn_exp2f(st.x - ref);
+    m = next;
+    l = l * old + st.y * by;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = v[j] * old + y.cols[((at * NB + b) * 4 + j) * kWave + lane] * by;
+  }
+  if (row >= rows) return;
+  const int token = row / a.group;
+  const int64_t at = static_cast<int64_t>(q.row + token) * a.heads + h * a.group + row - token * a.group;
+  const float inverse = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float out[4] = {v[j][0] * inverse, v[j][1] * inverse, v[j][2] * inverse, v[j][3] * inverse};
+    store4(a.y, a.y_dt, at * (NB * kQK) + b * kQK + 8 * j + 4 * half, out);
+  }
+  if (a.lse != nullptr && half == 0 && b == 0) a.lse[at] = l > 0.f ? (m - kLift2 + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// Heads of more than 128 values leave registers for half as many wavefronts.
+int wavefronts(int dim) { return dim > 128 ? 4 : 8; }
+
+int64_t places_of(const Attention& a) {
+  return static_cast<int64_t>(a.batch.tokens) * a.group / (32 * wavefronts(a.cache.dim)) + a.batch.seqs;
+}
+
+int splits_of(const Attention& a) {
+  const int64_t n = places_of(a) * a.cache.kv_heads, cu = device_cu_count();
+  return n >= cu ? 1 : static_cast<int>(cu / n < 32 ? cu / n : 32);
+}
+
+size_t stats_bytes(const Attention& a, int splits) {
+  return static_cast<size_t>(places_of(a)) * a.cache.kv_heads * splits * 32 * wavefronts(a.cache.dim) * 8;
+}
+
+std::atomic<uint64_t> g_allowed[8][2];
+
+template <int NB, bool BF16>
+hipError_t launch_as(const Attention& a, Many& y, Queue q) {
+  constexpr int kWaves = NB > 4 ? 4 : 8;
+  constexpr int kLds = 2 * (kTile * 4 * NB + NB * kQK * 8) * 16 + 32;
+  Attention args = a;
+  int64_t places = places_of(a);
+  void* argv[] = {&args, &y, &places};
+  const hipError_t e = launch_blocks(reinterpret_cast<const void*>(&attention_many_kernel<NB, kWaves, BF16>),
+                                     places * a.cache.kv_heads * y.splits, kWaves * kWave, argv, kLds, q, 1, 1, kLds,
+                                     &g_allowed[NB - 1][BF16]);
+  if (e != hipSuccess || y.splits == 1) return e;
+  return launch_blocks(reinterpret_cast<const void*>(&attention_splits_kernel<NB, kWaves>),
+                       places * a.cache.kv_heads, kWave, argv, 0, q, kWaves * NB);
+}
+
+template <int NB>
+hipError_t launch_dim(const Attention& a, Many& y, Queue q) {
+  return a.qt == DType::BF16 ? launch_as<NB, true>(a, y, q) : launch_as<NB, false>(a, y, q);
+}
+
+}  // namespace
+
+size_t attention_many_bytes(const Attention& a) {
+  const int splits = splits_of(a);
+  if (splits == 1) return 0;
+  return stats_bytes(a, splits) +
+         static_cast<size_t>(places_of(a)) * a.cache.kv_heads * splits * 32 * wavefronts(a.cache.dim) * a.cache.dim * 4;
+}
+
+hipError_t launch_attention_many(const Attention& a, int min_rows, void* workspace, Queue q) {
+  Many y;
+  y.min_rows = min_rows;
+  y.splits = splits_of(a);
+  y.stats = static_cast<float*>(workspace);
+  y.cols = reinterpret_cast<float4_t*>(behind(workspace, stats_bytes(a, y.splits)));
+  switch (a.cache.dim / kQK) {
+    case 1: return launch_dim<1>(a, y, q);
+    case 2: return launch_dim<2>(a, y, q);
+    case 3: return launch_dim<3>(a, y, q);
+    case 4: return launch_dim<4>(a, y, q);
+    case 5: return launch_dim<5>(a, y, q);
+    case 6: return launch_dim<6>(a, y, q);
+    case 7: return launch_dim<7>(a, y, q);
+    default: return launch_dim<8>(a, y, q);
+  }
+}
+
+}  // namespace q4

@@ -13,7 +13,8 @@ Errors of attention (`attention64`), with u = 2^-24 and w_t the softmax weights:
     exponent's argument 4 of the score and of the maximum;
   - a weight: relatively its score's error, 8 u for exp and, on matrix cores, 2^-11 for
     fp16 (2^-22 in two parts, of which the lower one's own grain is 2^-24 too), with a
-    floor of 2^-36 of the largest weight where fp16 has no more bits, in fp32 of 2^-126: a
+    floor of 2^-33 of the largest weight where fp16 has no more bits (half its subnormal
+    step, 2^-25, of weights that are lifted by 2^8 or more), in fp32 of 2^-126: a
     weight below 2^-126 of the largest (which is exp(0) = 1) is below fp32's normal
     range, and whether it is kept on the subnormal grid or flushed, it moves by at most itself;
   - y: sum w_t (|v_t| + |y|) times the weights' errors, (n + 40) u sum w |v| for the
@@ -213,7 +214,7 @@ def attention64(q, cache, batch, scale=None, causal=True, window=0, softcap=0.0,
             ep = (es.exp() - 1).clamp_max(1.0) + 8 * U
             if matrix:
                 ep = ep + 2.0 ** -11
-            ew = w * ep + (2.0 ** -36 if matrix else 2.0 ** -126) * seen / total.clamp_min(1e-300)
+            ew = w * ep + (2.0 ** -33 if matrix else 2.0 ** -126) * seen / total.clamp_min(1e-300)
             size = w @ vh.abs()
             b = ew @ vh.abs() + ew.sum(-1, keepdim=True) * yh.abs()
             b = b + size * ((length + 40) * U + (2.0 ** -11 if matrix else 0.0))
@@ -223,7 +224,7 @@ def attention64(q, cache, batch, scale=None, causal=True, window=0, softcap=0.0,
             lse[mine, h] = big
             size = torch.where(some[:, 0], big.abs(), torch.zeros_like(big))
             el[mine, h] = (w * (ep - (2.0 ** -11 if matrix else 0))).sum(-1) + (length + 40) * U + 4 * U * size + (
-                length * 2.0 ** -36 if matrix else 0.0)
+                length * 2.0 ** -33 if matrix else 0.0)
     return y, eb, lse, el
 
 

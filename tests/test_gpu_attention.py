@@ -39,7 +39,7 @@ def test_one_token(q4lib, gpu, dtype, d, heads, kv):
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("page", [16, 32, 48, 128, 1024])
 @pytest.mark.parametrize("kw", [{}, dict(window=1), dict(window=50), dict(window=300, softcap=3.0),
-                                dict(causal=False), dict(causal=False, window=20), dict(scale=-0.3)])
+                                dict(causal=False), dict(causal=False, window=20), dict(scale=-0.3), dict(scale=0.0)])
 def test_few_rows(q4lib, gpu, dtype, page, kw):
     """Drafts of several tokens, sequences without rows and with more rows than positions,
     rows before the first and behind the last sequence."""
@@ -49,7 +49,7 @@ def test_few_rows(q4lib, gpu, dtype, page, kw):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("d,heads,kv", [(128, 10, 2), (64, 3, 3), (96, 8, 1), (256, 4, 2), (32, 2, 1), (192, 6, 2)])
-@pytest.mark.parametrize("kw", [{}, dict(window=70), dict(softcap=5.0), dict(causal=False)])
+@pytest.mark.parametrize("kw", [{}, dict(window=70), dict(softcap=5.0), dict(causal=False), dict(scale=-0.2, window=40), dict(scale=0.0)])
 def test_many_rows(q4lib, gpu, dtype, d, heads, kv, kw):
     """Prompts, a chunk behind a history, and single tokens among them."""
     b = Batch([130, 61, 400, 300], [130, 61, 90, 1], 32, seed=d, before=2, behind=1)
