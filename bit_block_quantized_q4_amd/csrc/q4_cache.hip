@@ -3,6 +3,8 @@
 // A workgroup takes one granule (sixteen positions) of one sequence and kv head,
 // keys and values.  Grids are sized from the numbers of rows and sequences alone
 // (granule_places); what a place holds is found on the device.
+#include <type_traits>
+
 #include "q4_cache.hpp"
 #include "q4_quantize_block.hpp"
 
@@ -10,30 +12,6 @@ namespace q4 {
 namespace {
 
 constexpr int kThreads = 256;
-
-// Four consecutive elements, as fp32 (exact).
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, float (&v)[4]);
-template <>
-__device__ __forceinline__ void load4<float>(const float* p, float (&v)[4]) {
-  const float4_t t = *reinterpret_cast<const float4_t*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = t[i];
-}
-template <>
-__device__ __forceinline__ void load4<half_t>(const half_t* p, float (&v)[4]) {
-  const half4_t t = *reinterpret_cast<const half4_t*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(t[i]);
-}
-template <>
-__device__ __forceinline__ void load4<bf16_t>(const bf16_t* p, float (&v)[4]) {
-  const uint2 t = *reinterpret_cast<const uint2*>(p);
-  v[0] = bf16_bits_to_float(t.x & 0xFFFFu);
-  v[1] = bf16_bits_to_float(t.x >> 16);
-  v[2] = bf16_bits_to_float(t.y & 0xFFFFu);
-  v[3] = bf16_bits_to_float(t.y >> 16);
-}
 
 // Finite, of at most fp16's largest magnitude: NaN counts as 0.
 __device__ __forceinline__ float storable(float v) {
@@ -44,6 +22,7 @@ __device__ __forceinline__ float storable(float v) {
 // sequence s, the rows from `row` on.  False: nothing.
 struct Granule {
   int s, g, from, to, row;
+  int none, none_row;  // at a sequence's first place: its rows without a position
 };
 __device__ __forceinline__ bool granule_of(const Batch& b, int64_t place, Granule* out) {
   const int s = b.offsets == nullptr
@@ -51,7 +30,10 @@ __device__ __forceinline__ bool granule_of(const Batch& b, int64_t place, Granul
                     : last_not_above(b.seqs, place, [&](int i) { return granule_place(b, i); });
   const Seq q = seq_of(b, s);
   const int first = q.first < 0 ? 0 : q.first;  // the first position with a row
-  const int64_t g = first / kGranule + (b.offsets == nullptr ? 0 : place - granule_place(b, s));
+  const int64_t nth = b.offsets == nullptr ? 0 : place - granule_place(b, s);
+  const int64_t g = first / kGranule + nth;
+  out->none = q.first < 0 && nth == 0 ? (-q.first < q.rows ? -q.first : q.rows) : 0;
+  out->none_row = q.row;
   if (q.rows == 0 || g * kGranule >= q.length) return false;
   out->s = s;
   out->g = static_cast<int>(g);
@@ -62,117 +44,264 @@ __device__ __forceinline__ bool granule_of(const Batch& b, int64_t place, Granul
   return out->from < out->to;
 }
 
-// Eight lanes to a block of 32 values.  Keys' code bytes leave as words of a
-// position, values' as single bytes, sixteen positions apart.
+// ------------------------------------------------------------------ writing
+
+// Sixteen consecutive elements of a row, as fp32 (exact), limited to what is stored.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void cache_write_kernel(Cache c, Batch b, const T* __restrict__ k,
-                                                               int64_t k_stride, const T* __restrict__ v,
-                                                               int64_t v_stride) {
+__device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
+  constexpr int kPieces = sizeof(T);  // of 16 bytes
+  u32x4 w[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      v[i] = __builtin_bit_cast(float, static_cast<uint32_t>(w[i / 4][i % 4]));
+    } else {
+      const uint32_t two = w[i / 8][i / 2 % 4];
+      const uint32_t bits = i % 2 ? two >> 16 : two & 0xFFFFu;
+      if constexpr (std::is_same<T, half_t>::value) v[i] = half_bits_to_float(static_cast<uint16_t>(bits));
+      else v[i] = bf16_bits_to_float(bits);
+    }
+    v[i] = storable(v[i]);
+  }
+}
+
+// The Q4_0 rule on two lanes, 0 and 1 of a pair holding elements 0 .. 15 and 16 .. 31.
+// Returns the scale; words[0 .. 1] are this lane's code bytes, 0 .. 7 or 8 .. 15.
+//   m: the larger of max and -min; where they are equal the one that comes first.
+//   code: trunc(x / d + 8.5).  t = fma(x, 1 / d, 8.5) differs from the rule's t, two
+//   roundings, by less than 2^-17 (|x / d| <= 8.01; the reciprocal is good to 2^-23),
+//   so only a t within 2^-16 of an integer can truncate differently: those blocks redo
+//   the rule's own division.
+__device__ __forceinline__ half_t quantize_pair(int upper, const float (&v)[16], uint32_t (&words)[2]) {
+  float most = v[0], least = v[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) {
+    most = fmaxf(most, v[i]);
+    least = fminf(least, v[i]);
+  }
+  most = fmaxf(most, dpp_f<kDppXor1>(most));
+  least = fminf(least, dpp_f<kDppXor1>(least));
+  float m = most > -least ? most : least;
+  if (most == -least) {  // both signs, or zeros
+    int at = 99;
+    float found = 0.f;
+#pragma unroll
+    for (int i = 15; i >= 0; --i)
+      if (fabsf(v[i]) == most) {
+        at = i + 16 * upper;
+        found = v[i];
+      }
+    const int other = dpp_i<kDppXor1>(at);
+    const float theirs = dpp_f<kDppXor1>(found);
+    m = at < other ? found : theirs;
+  }
+  float t = m / -8.0f;  // (exact; kept from fusing with the rounding, as in quantize_lanes)
+  asm volatile("" : "+v"(t));
+  const half_t dh = static_cast<half_t>(t);
+  const float D = static_cast<float>(dh);
+  uint32_t code[4] = {0x08080808u, 0x08080808u, 0x08080808u, 0x08080808u};
+  if (D != 0.f) {
+    const float r = __builtin_amdgcn_rcpf(D);
+    float near = 1.f;
+    uint32_t q[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float u = fmaf(v[i], r, 8.5f);
+      near = fminf(near, fabsf(u - __builtin_rintf(u)));
+      const int c = static_cast<int>(u);
+      q[i] = static_cast<uint32_t>(c < 0 ? 0 : c > 15 ? 15 : c);
+    }
+    if (near < 0x1p-16f) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float e = v[i] / D;
+        asm volatile("" : "+v"(e));
+        const int c = static_cast<int>(e + 8.5f);
+        q[i] = static_cast<uint32_t>(c < 0 ? 0 : c > 15 ? 15 : c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) code[i] = q[4 * i] | q[4 * i + 1] << 8 | q[4 * i + 2] << 16 | q[4 * i + 3] << 24;
+  }
+  // The lower lane keeps words 0 and 1 of the block and gets their high nibbles, the
+  // upper lane words 2 and 3 and their low ones.
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t mine = upper ? code[2 + i] : code[i], give = upper ? code[i] : code[2 + i];
+    const uint32_t theirs = static_cast<uint32_t>(dpp_i<kDppXor1>(static_cast<int>(give)));
+    words[i] = upper ? theirs | mine << 4 : mine | theirs << 4;
+  }
+  return dh;
+}
+
+// Two lanes to a block of 32 values.  Code bytes and scales are put together as the
+// granule's image in LDS; a whole granule then leaves in 16-byte pieces, a part of one
+// as what belongs to its positions: words of a key, single bytes of values.
+template <typename T, int THREADS>
+__global__ __launch_bounds__(THREADS) void cache_write_kernel(Cache c, Batch b, const T* __restrict__ k,
+                                                              int64_t k_stride, const T* __restrict__ v,
+                                                              int64_t v_stride) {
+  __shared__ __attribute__((aligned(16))) uint8_t image[2][9 * 256];
   const int64_t place = blockIdx.x / c.kv_heads;
   const int h = static_cast<int>(blockIdx.x - place * c.kv_heads);
   Granule gr;
   if (!granule_of(b, place, &gr)) return;
   uint8_t* const keys = granule_at(c, b, gr.s, gr.g, h);
   if (keys == nullptr) return;
-  uint8_t* const values = keys + static_cast<int64_t>(c.per_page) * (9 * c.dim);
-  const int nb = c.dim / kQK, part = threadIdx.x & 7;
+  const int64_t to_values = static_cast<int64_t>(c.per_page) * (9 * c.dim);
+  const int nb = c.dim / kQK, upper = threadIdx.x & 1;
   const int n = gr.to - gr.from, tasks = 2 * n * nb;
-  for (int t = threadIdx.x >> 3; t < tasks; t += kThreads / 8) {
+  for (int t = threadIdx.x >> 1; t < tasks; t += THREADS / 2) {
     const bool value = t >= n * nb;
     const int u = value ? t - n * nb : t;
     const int i = u / nb, blk = u - i * nb, at = gr.from + i;
     const int64_t row = gr.row + i;
-    float x[4];
-    load4(value ? v + row * v_stride + h * c.dim + blk * kQK + part * 4
-                : k + row * k_stride + h * c.dim + blk * kQK + part * 4, x);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = storable(x[e]);
-    uint32_t bytes;
-    const half_t d = quantize_lanes(part, x, &bytes);
-    const uint16_t bits = __builtin_bit_cast(uint16_t, d);
+    float x[16];
+    load16((value ? v + row * v_stride : k + row * k_stride) + h * c.dim + blk * kQK + 16 * upper, x);
+    uint32_t words[2];
+    const uint16_t bits = __builtin_bit_cast(uint16_t, quantize_pair(upper, x, words));
+    uint8_t* const g = image[value];
+    uint16_t* const scales = reinterpret_cast<uint16_t*>(g + 8 * c.dim);
     if (value) {
-      if (part < 4) {
-        uint8_t* p = values + (blk * 16 + part * 4) * 16 + at;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[16 * e] = static_cast<uint8_t>(bytes >> (8 * e));
-      }
-      const int quarter = at & 3, place4 = (quarter & 1) * 2 + (quarter >> 1);
-      if (part == 0)
-        reinterpret_cast<uint16_t*>(values + 8 * c.dim)[blk * 16 + (at & ~3) + place4] = bits;
+      for (int e = 0; e < 8; ++e)
+        g[(blk * 16 + 8 * upper + e) * 16 + at] = static_cast<uint8_t>(words[e >> 2] >> (8 * (e & 3)));
+      const int quarter = at & 3;
+      if (upper == 0) scales[blk * 16 + (at & ~3) + (quarter & 1) * 2 + (quarter >> 1)] = bits;
     } else {
-      if (part < 4) *reinterpret_cast<uint32_t*>(keys + at * (c.dim / 2) + (part * nb + blk) * 4) = bytes;
-      if (part == 0) reinterpret_cast<uint16_t*>(keys + 8 * c.dim)[((at >> 2) * nb + blk) * 4 + (at & 3)] = bits;
-    }
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ T narrow(float v);
-template <>
-__device__ __forceinline__ float narrow<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ half_t narrow<half_t>(float v) { return static_cast<half_t>(v); }
-template <>
-__device__ __forceinline__ bf16_t narrow<bf16_t>(float v) {
-  return bf16_t{__builtin_bit_cast(uint16_t, static_cast<__bf16>(v))};
-}
-
-// One value of a granule in LDS.
-__device__ __forceinline__ float decoded(const uint8_t* g, bool value, int nb, int at, int e) {
-  const int blk = e / kQK, i = e & 15, high = (e >> 4) & 1;
-  const int quarter = at & 3;
-  const int code_at = value ? (blk * 16 + i) * 16 + at : at * nb * 16 + ((i >> 2) * nb + blk) * 4 + (i & 3);
-  const int scale_at = value ? blk * 16 + (at & ~3) + (quarter & 1) * 2 + (quarter >> 1)
-                             : ((at >> 2) * nb + blk) * 4 + quarter;
-  const int code = (g[code_at] >> (4 * high)) & 15;
-  const float d = half_bits_to_float(reinterpret_cast<const uint16_t*>(g + nb * 256)[scale_at]);
-  return static_cast<float>(code - 8) * d;
-}
-
-// A granule's bytes go through LDS; a thread gives eight values of a row at a time.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void cache_read_kernel(Cache c, Batch b, T* __restrict__ k,
-                                                              T* __restrict__ v) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][9 * 256];
-  const int64_t place = blockIdx.x / c.kv_heads;
-  const int h = static_cast<int>(blockIdx.x - place * c.kv_heads);
-  Granule gr;
-  if (!granule_of(b, place, &gr)) return;
-  const uint8_t* const keys = granule_at(c, b, gr.s, gr.g, h);
-  const int nb = c.dim / kQK, pieces = 9 * c.dim / 16;
-  if (keys != nullptr) {
-    const uint8_t* const values = keys + static_cast<int64_t>(c.per_page) * (9 * c.dim);
-    for (int i = threadIdx.x; i < 2 * pieces; i += kThreads) {
-      const int w = i >= pieces, j = i - w * pieces;
-      *reinterpret_cast<uint4*>(lds[w] + 16 * j) = *reinterpret_cast<const uint4*>((w ? values : keys) + 16 * j);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<uint32_t*>(g + at * (c.dim / 2) + ((2 * upper + e) * nb + blk) * 4) = words[e];
+      if (upper == 0) scales[((at >> 2) * nb + blk) * 4 + (at & 3)] = bits;
     }
   }
   __syncthreads();
-  const int n = gr.to - gr.from, per_row = c.dim / 8;
-  const int64_t row_elems = static_cast<int64_t>(c.kv_heads) * c.dim;
-  for (int t = threadIdx.x; t < 2 * n * per_row; t += kThreads) {
-    const bool value = t >= n * per_row;
-    const int u = value ? t - n * per_row : t;
-    const int i = u / per_row, e = (u - i * per_row) * 8;
-    T out[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      out[j] = narrow<T>(keys == nullptr ? 0.f : decoded(lds[value], value, nb, gr.from + i, e + j));
-    T* const p = (value ? v : k) + (gr.row + i) * row_elems + h * c.dim + e;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = out[j];
+  if (n == kGranule) {
+    const int pieces = 9 * c.dim / 16;
+    for (int i = threadIdx.x; i < 2 * pieces; i += THREADS) {
+      const int w = i >= pieces, j = i - w * pieces;
+      *reinterpret_cast<u32x4*>(keys + w * to_values + 16 * j) = *reinterpret_cast<const u32x4*>(image[w] + 16 * j);
+    }
+    return;
+  }
+  const int words = n * nb * 4;  // a key's code words lie together
+  for (int i = threadIdx.x; i < words; i += THREADS) {
+    const int at = gr.from * nb * 4 + i;
+    reinterpret_cast<uint32_t*>(keys)[at] = reinterpret_cast<const uint32_t*>(image[0])[at];
+  }
+  for (int i = threadIdx.x; i < n * nb * 16; i += THREADS) {
+    const int byte = i / n, at = byte * 16 + gr.from + i - byte * n;
+    keys[to_values + at] = image[1][at];
+  }
+  for (int i = threadIdx.x; i < 2 * n * nb; i += THREADS) {
+    const int w = i >= n * nb, u = i - w * n * nb, t = gr.from + u / nb, blk = u % nb, quarter = t & 3;
+    const int at = w ? blk * 16 + (t & ~3) + (quarter & 1) * 2 + (quarter >> 1) : ((t >> 2) * nb + blk) * 4 + quarter;
+    reinterpret_cast<uint16_t*>(keys + w * to_values + 8 * c.dim)[at] =
+        reinterpret_cast<const uint16_t*>(image[w] + 8 * c.dim)[at];
   }
 }
 
-// Rows of a sequence whose position is negative (fewer positions than rows).
+// ------------------------------------------------------------------ reading
+
+// Eight values (q - 8) d, rounded to T, from two dwords whose bytes' low or (high)
+// nibbles are the codes; stored as 16-byte pieces.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void cache_read_none_kernel(Batch b, int64_t row_elems, T* __restrict__ k,
-                                                                   T* __restrict__ v) {
-  for (int s = blockIdx.x; s < b.seqs; s += gridDim.x) {
-    const Seq q = seq_of(b, s);
-    const int64_t n = q.first < 0 ? (-q.first < q.rows ? -q.first : q.rows) * row_elems : 0;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads)
-      k[q.row * row_elems + i] = v[q.row * row_elems + i] = narrow<T>(0.f);
+__device__ __forceinline__ void give8(T* p, uint32_t w0, uint32_t w1, bool high, float d) {
+  const int by = high ? 4 : 0;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = i < 4 ? w0 : w1;
+    v[i] = static_cast<float>(static_cast<int>((w >> (8 * (i & 3) + by)) & 15u) - 8) * d;
+  }
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4_t*>(p)[0] = float4_t{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<float4_t*>(p)[1] = float4_t{v[4], v[5], v[6], v[7]};
+  } else {
+    constexpr int dt = static_cast<int>(std::is_same<T, half_t>::value ? DType::F16 : DType::BF16);
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = f32_to_16(v[2 * i], dt) | static_cast<uint32_t>(f32_to_16(v[2 * i + 1], dt)) << 16;
+    *reinterpret_cast<u32x4*>(p) = o;
+  }
+}
+
+// 4 x 4 bytes turned: byte j of out[i] is byte i of in[j].
+__device__ __forceinline__ void turn4(const uint32_t (&in)[4], uint32_t (&out)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(in[1], in[0], 0x05010400), b = __builtin_amdgcn_perm(in[1], in[0], 0x07030602);
+  const uint32_t c = __builtin_amdgcn_perm(in[3], in[2], 0x05010400), d = __builtin_amdgcn_perm(in[3], in[2], 0x07030602);
+  out[0] = __builtin_amdgcn_perm(c, a, 0x05040100);
+  out[1] = __builtin_amdgcn_perm(c, a, 0x07060302);
+  out[2] = __builtin_amdgcn_perm(d, b, 0x05040100);
+  out[3] = __builtin_amdgcn_perm(d, b, 0x07060302);
+}
+
+// A thread takes eight values of a key, or of four positions' values (whose bytes lie
+// sixteen apart: eight words of four positions each, turned in registers), for
+// `per` kv heads in turn.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void cache_read_kernel(Cache c, Batch b, T* __restrict__ k, T* __restrict__ v,
+                                                              int per, int chunks) {
+  const int64_t place = blockIdx.x / chunks;
+  const int h0 = static_cast<int>(blockIdx.x - place * chunks) * per;
+  const int heads = c.kv_heads - h0 < per ? c.kv_heads - h0 : per;
+  const int64_t row_elems = static_cast<int64_t>(c.kv_heads) * c.dim;
+  Granule gr;
+  const bool some = granule_of(b, place, &gr);
+  if (gr.none > 0) {  // the sequence's rows without a position, by its first place
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(gr.none) * heads * c.dim; i += kThreads) {
+      const int64_t row = i / (heads * c.dim);
+      const int64_t at = (gr.none_row + row) * row_elems + h0 * c.dim + (i - row * heads * c.dim);
+      k[at] = v[at] = T{};
+    }
+  }
+  if (!some) return;
+  const uint8_t* const keys = granule_at(c, b, gr.s, gr.g, h0);
+  const int64_t to_values = static_cast<int64_t>(c.per_page) * (9 * c.dim);
+  const int nb = c.dim / kQK, n = gr.to - gr.from;
+  const int key_tasks = n * nb * 4, value_tasks = nb * 16;  // of a head
+  for (int t = threadIdx.x; t < heads * (key_tasks + value_tasks); t += kThreads) {
+    if (t < heads * key_tasks) {  // (position, head, block, eight values): as they lie in k
+      const int i = t / (heads * nb * 4), e = t - i * (heads * nb * 4), h = e / (nb * 4);
+      const int blk = e / 4 - h * nb, part = e & 3, at = gr.from + i;
+      T* const p = k + (gr.row + i) * row_elems + h0 * c.dim + e * 8;
+      uint32_t w[2] = {0, 0};
+      float d = 0.f;
+      if (keys != nullptr) {
+        const uint8_t* g = keys + h * c.head_bytes;
+        const int word = 2 * (part & 1);
+        w[0] = *reinterpret_cast<const uint32_t*>(g + at * (c.dim / 2) + (word * nb + blk) * 4);
+        w[1] = *reinterpret_cast<const uint32_t*>(g + at * (c.dim / 2) + ((word + 1) * nb + blk) * 4);
+        d = half_bits_to_float(reinterpret_cast<const uint16_t*>(g + 8 * c.dim)[((at >> 2) * nb + blk) * 4 + (at & 3)]);
+      }
+      give8<T>(p, w[0], w[1], part >= 2, d);
+    } else {  // (head, block, half of its bytes, nibble, four positions)
+      const int r = t - heads * key_tasks, h = r / value_tasks, e = r - h * value_tasks;
+      const int u = e & 3, part = (e >> 2) & 3, blk = e >> 4;
+      if (4 * u + 4 <= gr.from || 4 * u >= gr.to) continue;
+      uint32_t in[2][4] = {}, out[2][4];
+      uint2 sc = {0, 0};
+      if (keys != nullptr) {
+        const uint8_t* g = keys + h * c.head_bytes + to_values;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          in[i / 4][i % 4] = *reinterpret_cast<const uint32_t*>(g + (blk * 16 + 8 * (part & 1) + i) * 16 + 4 * u);
+        sc = *reinterpret_cast<const uint2*>(g + 8 * c.dim + blk * 32 + u * 8);  // positions 0, 2, 1, 3
+      }
+      turn4(in[0], out[0]);
+      turn4(in[1], out[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = 4 * u + i;
+        if (at < gr.from || at >= gr.to) continue;
+        const uint32_t two = i & 1 ? sc.y : sc.x;
+        const float d = half_bits_to_float(static_cast<uint16_t>(i & 2 ? two >> 16 : two));
+        give8<T>(v + (gr.row + at - gr.from) * row_elems + (h0 + h) * c.dim + blk * kQK + part * 8, out[0][i],
+                 out[1][i], part >= 2, d);
+      }
+    }
   }
 }
 
@@ -183,8 +312,10 @@ hipError_t write_as(const Cache& c, const Batch& b, const void* k, int64_t k_str
   Batch ba = b;
   const T *kp = static_cast<const T*>(k), *vp = static_cast<const T*>(v);
   void* argv[] = {&ca, &ba, &kp, &k_stride, &vp, &v_stride};
-  return launch_blocks(reinterpret_cast<const void*>(&cache_write_kernel<T>), granule_places(b) * c.kv_heads,
-                       kThreads, argv, 0, q);
+  const int64_t n = granule_places(b) * c.kv_heads;
+  if (b.offsets == nullptr)  // one position each: a wavefront has lanes for it
+    return launch_blocks(reinterpret_cast<const void*>(&cache_write_kernel<T, kWave>), n, kWave, argv, 0, q);
+  return launch_blocks(reinterpret_cast<const void*>(&cache_write_kernel<T, kThreads>), n, kThreads, argv, 0, q);
 }
 
 template <typename T>
@@ -192,14 +323,13 @@ hipError_t read_as(const Cache& c, const Batch& b, void* k, void* v, Queue q) {
   Cache ca = c;
   Batch ba = b;
   T *kp = static_cast<T*>(k), *vp = static_cast<T*>(v);
-  void* argv[] = {&ca, &ba, &kp, &vp};
-  const hipError_t e = launch_blocks(reinterpret_cast<const void*>(&cache_read_kernel<T>),
-                                     granule_places(b) * c.kv_heads, kThreads, argv, 0, q);
-  if (e != hipSuccess) return e;
-  int64_t row_elems = static_cast<int64_t>(c.kv_heads) * c.dim;
-  void* none[] = {&ba, &row_elems, &kp, &vp};
-  return launch_blocks(reinterpret_cast<const void*>(&cache_read_none_kernel<T>), b.seqs < 1024 ? b.seqs : 1024,
-                       kThreads, none, 0, q);
+  // Heads that a workgroup takes in turn: eight where there are plenty of granules.
+  const int64_t places = granule_places(b), plenty = places * c.kv_heads / (8 * static_cast<int64_t>(device_cu_count()));
+  int per = plenty < 1 ? 1 : plenty < 8 ? static_cast<int>(plenty) : 8;
+  if (per > c.kv_heads) per = c.kv_heads;
+  int chunks = (c.kv_heads + per - 1) / per;
+  void* argv[] = {&ca, &ba, &kp, &vp, &per, &chunks};
+  return launch_blocks(reinterpret_cast<const void*>(&cache_read_kernel<T>), places * chunks, kThreads, argv, 0, q);
 }
 
 }  // namespace
