@@ -308,7 +308,9 @@ def _own(s):
         return {"y": out[0], "lse": out[1]} if c["lse"] else {"y": out}
     if c["op"] == "store":
         q4.q4_cache_write(s["k"], s["v"], s["cache"], s["tables"], s["lengths"], s["offsets"])
-    tokens = sum(_lengths(c)[1])
+        tokens = s["k"].shape[0]
+    else:
+        tokens = sum(_lengths(c)[1])
     k, v = q4.q4_cache_read(s["cache"], s["tables"], s["lengths"], s["offsets"], tokens=tokens,
                             dtype=_TYPES[c["dtype"]])
     return {"k": k, "v": v}
