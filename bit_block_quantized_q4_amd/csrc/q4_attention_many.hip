@@ -20,6 +20,8 @@
 //
 // Where there are fewer workgroups than compute units the positions are split as well,
 // and the parts joined in a second launch.
+#include <type_traits>
+
 #include "q4_attention.hpp"
 
 namespace q4 {
@@ -64,6 +66,18 @@ __device__ __forceinline__ bool job_of(const Attention& a, const Many& y, int64_
   return true;
 }
 
+// What position t's piece numbers are exclusive-ored with.  LDS serves sixteen lanes at
+// a time from 256 bytes of banks; rows are 64 NB bytes.  Read are sixteen positions'
+// pieces of one number, written four positions' of four.
+template <int NB>
+__device__ __forceinline__ int turn_key(int t) {
+  if constexpr (NB % 4 == 0) return (t & 3) << 2 | (t >> 2 & 3);
+  else if constexpr (NB % 2 == 0) return (t >> 1 & 1) << 2 | (t >> 2 & 3);
+  else return t >> 2 & 3;
+}
+// As that for column c's, of 128 bytes.
+__device__ __forceinline__ int turn_value(int c) { return c >> 1 & 7; }
+
 template <int NB>
 struct Bytes {
   uint32_t k[NB];
@@ -71,11 +85,24 @@ struct Bytes {
   u32x4 v[(NB + 3) / 4], vs[(NB + 3) / 4][2];
 };
 
+// The order of N LDS reads and as many matrix products behind it: kAhead reads go ahead
+// (left alone the compiler reads two pieces, waits, and multiplies).
+constexpr int kAhead = 4;
+template <int N>
+__device__ __forceinline__ void feed() {
+  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+  for (int i = 0; i < N - kAhead; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+}
+
 template <int NB, int WAVES, bool BF16>
 __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel(Attention a, Many y, int64_t places) {
   constexpr int R = 32 * WAVES;
   constexpr int kPieces = 4 * NB;                 // of a position's key
-  constexpr int kSwizzle = NB % 4 == 0 ? 15 : NB % 2 == 0 ? 7 : 3;  // 4 NB is a multiple of one more
   constexpr int kKeys = kTile * kPieces, kValues = NB * kQK * 8;
   extern __shared__ __attribute__((aligned(16))) uint8_t dynamic[];
   // [2] buffers of keys and values, then [2][4] whether a granule has a page
@@ -171,17 +198,30 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
   const int64_t to_values = static_cast<int64_t>(c.per_page) * (288 * NB);
   Bytes<NB> bytes;
   int fetched_named = 0;
-  auto fetch = [&](int tile) {
-    const uint32_t gi = static_cast<uint32_t>(tile * 4 + mine), per = static_cast<uint32_t>(c.per_page);
-    uint32_t slot = __umulhi(gi, c.inverse), in = gi - slot * per;
-    if (in >= per) {
+  // Where the granule of a tile lies, for 64 tiles at a time, one a lane (its upper half
+  // all ones: nowhere).
+  uint32_t at_lo = 0, at_hi = 0;
+  auto look_up = [&](int tile) __attribute__((always_inline)) {
+    const uint32_t gi = static_cast<uint32_t>((tile + lane) * 4 + mine), per = static_cast<uint32_t>(c.per_page);
+    uint32_t slot = __umulhi(gi, c.inverse), inside = gi - slot * per;
+    if (inside >= per) {
       ++slot;
-      in -= per;
+      inside -= per;
     }
-    const int id = slot < static_cast<uint32_t>(a.batch.max_pages) ? table[slot] : -1;
-    fetched_named = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.pages);
-    const uint8_t* p = c.data + (fetched_named ? id : 0) * c.page_bytes + h * c.head_bytes +
-                       static_cast<int64_t>(in) * (288 * NB);
+    int id = -1;
+    if (tile + lane < t1 && slot < static_cast<uint32_t>(a.batch.max_pages)) id = table[slot];
+    const uint64_t at = static_cast<uint64_t>(id) * c.page_bytes + static_cast<uint64_t>(inside) * (288 * NB);
+    const bool some = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.pages);
+    at_lo = static_cast<uint32_t>(at);
+    at_hi = some ? static_cast<uint32_t>(at >> 32) : ~0u;
+  };
+  const uint8_t* const head = c.data + h * c.head_bytes;
+  auto fetch = [&](int tile) __attribute__((always_inline)) {
+    const int i = (tile - t0) & 63;
+    if (i == 0) look_up(tile);
+    const uint32_t high = __builtin_amdgcn_readlane(at_hi, i), low = __builtin_amdgcn_readlane(at_lo, i);
+    fetched_named = high != ~0u;
+    const uint8_t* p = head + (fetched_named ? static_cast<uint64_t>(high) << 32 | low : 0);
     if (keys_here) {
       const uint32_t* w = reinterpret_cast<const uint32_t*>(p) + lane * NB;
 #pragma unroll
@@ -203,7 +243,8 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
       }
     }
   };
-  auto decode = [&](int tile, int buffer) {
+  auto decode = [&](int tile, auto parity) __attribute__((always_inline)) {
+    constexpr int buffer = decltype(parity)::value;
     u32x4* const keys = lds + buffer * (kKeys + kValues);
     u32x4* const values = keys + kKeys;
     if (keys_here) {
@@ -214,7 +255,7 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
         const half_t d = __builtin_bit_cast(half_t, bytes.ks[b]);
         const half2_t dd = {d, d};
         const half8_t piece = join(k.l02 * dd, k.l13 * dd, k.h02 * dd, k.h13 * dd);
-        keys[t * kPieces + ((4 * b + g) ^ (t & kSwizzle))] = __builtin_bit_cast(u32x4, piece);
+        keys[t * kPieces + ((4 * b + g) ^ turn_key<NB>(t))] = __builtin_bit_cast(u32x4, piece);
       }
       if (lane == 0) named[buffer * 4 + mine] = fetched_named;
     }
@@ -245,8 +286,8 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
           const half2_t d3 = __builtin_bit_cast(half2_t, static_cast<uint32_t>(bytes.vs[i][1][2 * hf + 1]));
           const half8_t low = join(v0.l02 * d0, v0.l13 * d1, v1.l02 * d2, v1.l13 * d3);
           const half8_t high = join(v0.h02 * d0, v0.h13 * d1, v1.h02 * d2, v1.h13 * d3);
-          values[col * 8 + ((2 * mine + hf) ^ (col & 7))] = __builtin_bit_cast(u32x4, low);
-          values[(col + 16) * 8 + ((2 * mine + hf) ^ (col & 7))] = __builtin_bit_cast(u32x4, high);
+          values[col * 8 + ((2 * mine + hf) ^ turn_value(col))] = __builtin_bit_cast(u32x4, low);
+          values[(col + 16) * 8 + ((2 * mine + hf) ^ turn_value(col))] = __builtin_bit_cast(u32x4, high);
         }
       }
     }
@@ -259,98 +300,153 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
 
-  if (t0 < t1) {
-    fetch(t0);
-    decode(t0, 0);
-    if (t0 + 1 < t1) fetch(t0 + 1);
-    __syncthreads();
-  }
-  for (int t = t0; t < t1; ++t) {
-    const int buffer = (t - t0) & 1, first = t * kTile;
-    const bool seen = w0 < w1 && first < whi && first + kTile > wlo;
-    const u32x4* const keys = lds + buffer * (kKeys + kValues);
-    const u32x4* const values = keys + kKeys;
-    half8_t p[4];
-    if (seen) {
-      float16_t x[2];
+  half8_t p[4];
+  float16_t x[2];
+  int4 there = {0, 0, 0, 0};  // whether the tile's granules have pages
+  // The tiles that the wavefront's rows see some of, and those that each sees whole.
+  const int some0 = w0 < w1 ? wlo / kTile : t1, some1 = w0 < w1 ? (whi + kTile - 1) / kTile : 0;
+  const int whole0 = (wlo_last + kTile - 1) / kTile, whole1 = w1 == w0 + 32 ? whi_first / kTile : 0;
+  auto scores = [&](auto parity) __attribute__((always_inline)) {
+    const u32x4* const keys = lds + decltype(parity)::value * (kKeys + kValues);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[mt][i] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 2 * NB; ++ks)
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[mt][i] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < 2 * NB; ++ks) {
-          const half8_t kf = __builtin_bit_cast(
-              half8_t, keys[(32 * mt + n) * kPieces + ((2 * ks + half) ^ (n & kSwizzle))]);
-          x[mt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[ks], x[mt], 0, 0, 0);
-        }
+        const half8_t kf = __builtin_bit_cast(
+            half8_t, keys[(32 * mt + n) * kPieces + ((2 * ks + half) ^ turn_key<NB>(n))]);
+        x[mt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[ks], x[mt], 0, 0, 0);
       }
-      const int4 nm = *reinterpret_cast<const int4*>(named + 4 * buffer);
-      const bool all = (nm.x & nm.y & nm.z & nm.w) != 0;
-      float by = mul;
-      if (a.softcap > 0.f) {
-        by = 1.f;
+  };
+  auto products = [&](auto parity) __attribute__((always_inline)) {
+    const u32x4* const values = lds + decltype(parity)::value * (kKeys + kValues) + kKeys;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[mt][i] = cap.of(x[mt][i] * mul);
+      for (int b = 0; b < NB; ++b) {
+        const half8_t vf = __builtin_bit_cast(half8_t, values[(32 * b + n) * 8 + ((2 * k + half) ^ turn_value(n))]);
+        o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[k], o[b], 0, 0, 0);
       }
-      if (!(first >= wlo_last && first + kTile <= whi_first && all && w1 == w0 + 32)) {
-        const int from = lo - first - 4 * half, to = hi - first - 4 * half;
+  };
+  auto weights = [&](int t) __attribute__((always_inline)) {
+    const bool all = __builtin_amdgcn_readfirstlane(there.x & there.y & there.z & there.w) != 0;
+    float by = mul;
+    if (a.softcap > 0.f) {
+      by = 1.f;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int e = 32 * mt + 8 * (i / 4) + i % 4;
-            const int there = e / 16 == 0 ? nm.x : e / 16 == 1 ? nm.y : e / 16 == 2 ? nm.z : nm.w;
-            x[mt][i] = there && e >= from && e < to ? x[mt][i] : -INFINITY;
-          }
-      }
-      float top = fmaxf(x[0][0], x[1][0]);
+        for (int i = 0; i < 16; ++i) x[mt][i] = cap.of(x[mt][i] * mul);
+    }
+    if (!(t >= whole0 && t < whole1 && all)) {
+      const int first = t * kTile;
+      const int from = lo - first - 4 * half, to = hi - first - 4 * half;
 #pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(x[0][i], x[1][i]), top);
-      top = max_over_halves(top) * by;
-      if (__any(top > m + kSlack)) {
-        const float next = fmaxf(m, top);
-        const float old = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - next);
-        m = next;
-        l *= old;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[b][i] *= old;
-      }
-      const float from = kLift2 - (m == -INFINITY ? 0.f : m);
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          x[mt][i] = __builtin_amdgcn_exp2f(fmaf(x[mt][i], by, from));
-          l += x[mt][i];
+          const int e = 32 * mt + 8 * (i / 4) + i % 4;
+          const int page = e / 16 == 0 ? there.x : e / 16 == 1 ? there.y : e / 16 == 2 ? there.z : there.w;
+          x[mt][i] = page && e >= from && e < to ? x[mt][i] : -INFINITY;
         }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          constexpr int kOrder[8] = {0, 2, 1, 3, 4, 6, 5, 7};
-          half_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = static_cast<half_t>(x[mt][8 * ks + kOrder[e]]);
-          p[2 * mt + ks] = half8_t{w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
-        }
-      }
     }
-    if (t + 1 < t1) {
-      decode(t + 1, buffer ^ 1);
-      if (t + 2 < t1) fetch(t + 2);
-    }
-    if (seen) {
+    float top = fmaxf(x[0][0], x[1][0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(x[0][i], x[1][i]), top);
+    top = max_over_halves(top) * by;
+    if (__any(top > m + kSlack)) {
+      const float next = fmaxf(m, top);
+      const float old = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - next);
+      m = next;
+      l *= old;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const half8_t vf = __builtin_bit_cast(half8_t, values[(32 * b + n) * 8 + ((2 * k + half) ^ (n & 7))]);
-          o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[k], o[b], 0, 0, 0);
-        }
+        for (int i = 0; i < 16; ++i) o[b][i] *= old;
     }
-    __syncthreads();
+    const float from = kLift2 - (m == -INFINITY ? 0.f : m);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[mt][i] = __builtin_amdgcn_exp2f(fmaf(x[mt][i], by, from));
+        l += x[mt][i];
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        constexpr int kOrder[8] = {0, 2, 1, 3, 4, 6, 5, 7};
+        half_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = static_cast<half_t>(x[mt][8 * ks + kOrder[e]]);
+        p[2 * mt + ks] = half8_t{w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+      }
+    }
+  };
+  auto nothing = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[i][e] = static_cast<half_t>(0.f);
+  };
+  // A barrier that waits for this wavefront's LDS accesses alone: fetches stay in flight.
+  auto meet = [&]() __attribute__((always_inline)) {
+    wait_lgkm0();
+    __builtin_amdgcn_s_barrier();
+    compiler_fence();
+  };
+
+  // Two phases a tile, each ended by a barrier: products (the scores of tile t, the
+  // columns of t - 1), then weights of t and the decoding of t + 1.  The second four
+  // wavefronts, one on each SIMD beside one of the first four, run one phase behind, so
+  // that matrix and vector units work at the same time.  In phases of the first four
+  // (the second four one later): tile t's keys and the values of t - 1 are read in 2 t
+  // and 2 t + 1, keys of t + 1 (by the first four) written in 2 t + 1, values of t + 1 (by
+  // the second four) in 2 t + 2: two buffers of each do.
+  const int group = WAVES == 8 ? wave >> 2 : 0;
+  using Even = std::integral_constant<int, 0>;
+  using Odd = std::integral_constant<int, 1>;
+  if (t0 < t1) {
+    for (int i = threadIdx.x; i < kValues; i += WAVES * kWave)  // the values before the first tile
+      lds[kKeys + kValues + kKeys + i] = u32x4{0, 0, 0, 0};
+    fetch(t0);
+    decode(t0, Even());
+    if (t0 + 1 < t1) fetch(t0 + 1);
+    meet();
+    if (group == 1) meet();
+    bool before = false;  // tile t - 1 was seen: p holds its weights, else zeros
+    nothing();
+    auto step = [&](int t, auto mine_, auto other) __attribute__((always_inline)) {
+      const bool seen = t >= some0 && t < some1;
+      there = *reinterpret_cast<const int4*>(named + 4 * decltype(mine_)::value);
+      // (One block, so that reads and products of both run into each other: with no tile
+      // before, its weights are 0.)
+      if (seen || before) {
+        scores(mine_);
+        products(other);
+        feed<8 * NB>();
+      }
+      meet();
+      if (t + 1 < t1) {  // (first, so that its writes are through before the barrier)
+        decode(t + 1, other);
+        if (t + 2 < t1) fetch(t + 2);
+      }
+      if (seen) weights(t);
+      else nothing();
+      before = seen;
+      meet();
+    };
+    for (int t = t0; t < t1; t += 2) {
+      step(t, Even(), Odd());
+      if (t + 1 < t1) step(t + 1, Odd(), Even());
+    }
+    if (before) {
+      if ((t1 - 1 - t0) & 1) products(Odd());
+      else products(Even());
+    }
+    if (WAVES == 8 && group == 0) meet();
   }
 
   l = sum_over_halves(l);
