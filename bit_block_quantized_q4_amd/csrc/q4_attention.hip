@@ -10,7 +10,6 @@
 namespace q4 {
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kMaxDim = 256;
 // A workgroup per row and head; a wavefront takes every fourth tile of 64 positions:
 // first a position a lane (its score), then two pairs of columns a lane.  Everything
@@ -144,24 +143,14 @@ hipError_t launch_row(const Attention& a, Queue q) {
 
 }  // namespace
 
-// Most rows (query rows times heads per kv head) that a sequence has for the kernel of
-// few rows.
-constexpr int kFewRows = 32;
-
 size_t attention_workspace_bytes(const Attention& a) {
   if (a.qt == DType::F32) return 0;
-  const size_t few = attention_few_bytes(a);
-  return a.batch.offsets == nullptr ? few : (few + 255) / 256 * 256 + attention_many_bytes(a);
+  return a.batch.offsets == nullptr ? attention_few_bytes(a) : attention_mixed_bytes(a);
 }
 
-// Without offsets every sequence has the rows of one token.  With them their numbers are
-// on the device: both kernels are launched, and each takes the sequences that are its.
 hipError_t launch_attention(const Attention& a, void* workspace, Queue q) {
   if (a.qt == DType::F32) return launch_row(a, q);
-  if (a.batch.offsets == nullptr) return launch_attention_few(a, 1 << 30, workspace, q);
-  const hipError_t e = launch_attention_many(
-      a, kFewRows + 1, behind(workspace, (attention_few_bytes(a) + 255) / 256 * 256), q);
-  return e != hipSuccess ? e : launch_attention_few(a, kFewRows, workspace, q);
+  return a.batch.offsets == nullptr ? launch_attention_few(a, workspace, q) : launch_attention_mixed(a, workspace, q);
 }
 
 }  // namespace q4

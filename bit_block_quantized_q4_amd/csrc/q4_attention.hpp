@@ -10,6 +10,8 @@
 
 namespace q4 {
 
+constexpr int kTile = 64;  // positions
+constexpr int kWaves = 4;  // wavefronts of a workgroup
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLift = 12.f;
@@ -100,13 +102,10 @@ __device__ __forceinline__ void store4(void* y, int dt, int64_t at, const float 
   }
 }
 
-// Sequences of at most max_rows rows (query rows times heads per kv head).
+// Every sequence one row (no offsets), and any numbers of rows.
 size_t attention_few_bytes(const Attention& a);
-hipError_t launch_attention_few(const Attention& a, int max_rows, void* workspace, Queue q);
-
-
-// Sequences of at least min_rows.
-size_t attention_many_bytes(const Attention& a);
-hipError_t launch_attention_many(const Attention& a, int min_rows, void* workspace, Queue q);
+hipError_t launch_attention_few(const Attention& a, void* workspace, Queue q);
+size_t attention_mixed_bytes(const Attention& a);
+hipError_t launch_attention_mixed(const Attention& a, void* workspace, Queue q);
 
 }  // namespace q4

@@ -20,20 +20,20 @@
 //
 // Where there are fewer workgroups than compute units the positions are split as well,
 // and the parts joined in a second launch.
-#include <type_traits>
+#pragma once
 
 #include "q4_attention.hpp"
 
 namespace q4 {
-namespace {
 
-constexpr int kTile = 64;
+constexpr int kManyRows = 32 * kWaves;
 constexpr float kLift2 = 8.f;   // weights are held times 2^8 ..
 constexpr float kSlack = 7.f;   // .. of a maximum that may have grown by 2^7 since
 
 struct Many {
   int min_rows = 0;   // sequences of fewer rows are left out
   int splits = 1;
+  int64_t places = 0;
   float* stats = nullptr;   // [workgroups][rows][2]
   float4_t* cols = nullptr; // [workgroups][wavefronts][NB][4][64]
 };
@@ -47,13 +47,13 @@ __device__ __forceinline__ int64_t row_place(const Batch& b, int group, int rows
 // What workgroup `at` takes: heads inside (neighbours, which lie on other dies, then
 // read other keys), the last rows, which see most, first.
 template <int R>
-__device__ __forceinline__ bool job_of(const Attention& a, const Many& y, int64_t at, int64_t places, int* s, int* h,
+__device__ __forceinline__ bool job_of(const Attention& a, const Many& y, int64_t at, int* s, int* h,
                                        int* r0, int* rows, int* split, Seq* q) {
   const int kv = a.cache.kv_heads;
   *h = static_cast<int>(at % kv);
   at /= kv;
   *split = static_cast<int>(at % y.splits);
-  const int64_t place = places - 1 - at / y.splits;
+  const int64_t place = y.places - 1 - at / y.splits;
   *s = a.batch.offsets == nullptr ? static_cast<int>(place) : last_not_above(a.batch.seqs, place, [&](int i) {
     return row_place(a.batch, a.group, R, i);
   });
@@ -71,12 +71,12 @@ __device__ __forceinline__ bool job_of(const Attention& a, const Many& y, int64_
 // pieces of one number, written four positions' of four.
 template <int NB>
 __device__ __forceinline__ int turn_key(int t) {
-  if constexpr (NB % 4 == 0) return (t & 3) << 2 | (t >> 2 & 3);
-  else if constexpr (NB % 2 == 0) return (t >> 1 & 1) << 2 | (t >> 2 & 3);
+  if constexpr (NB % 4 == 0) return (t & 15) ^ (t & 1) << 2;
+  else if constexpr (NB % 2 == 0) return (t >> 1 & 3) | ((t ^ t >> 3) & 1) << 2;
   else return t >> 2 & 3;
 }
 // As that for column c's, of 128 bytes.
-__device__ __forceinline__ int turn_value(int c) { return c >> 1 & 7; }
+__device__ __forceinline__ int turn_value(int c) { return (c & 7) ^ (c >> 3 & 1); }
 
 template <int NB>
 struct Bytes {
@@ -87,34 +87,39 @@ struct Bytes {
 
 // The order of N LDS reads and as many matrix products behind it: kAhead reads go ahead
 // (left alone the compiler reads two pieces, waits, and multiplies).
-constexpr int kAhead = 4;
-template <int N>
+template <int N, int AHEAD>
 __device__ __forceinline__ void feed() {
-  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
 #pragma unroll
-  for (int i = 0; i < N - kAhead; ++i) {
+  for (int i = 0; i < N - AHEAD; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
   }
-  __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+  __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
 }
 
-template <int NB, int WAVES, bool BF16>
-__global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel(Attention a, Many y, int64_t places) {
-  constexpr int R = 32 * WAVES;
+template <int NB>
+struct ManyLds {
+  u32x4 tiles[2][kTile * 4 * NB + NB * kQK * 8];  // keys and values, in two buffers
+  int named[2][4];                                // whether a granule has a page
+};
+
+// Workgroup `block`.
+template <int NB, bool BF16>
+__device__ __forceinline__ void attention_many(const Attention& a, const Many& y, int64_t block, ManyLds<NB>& shared) {
+  constexpr int R = kManyRows;
+  constexpr int kAhead = NB > 6 ? 2 : 4;          // LDS reads before the first product
   constexpr int kPieces = 4 * NB;                 // of a position's key
   constexpr int kKeys = kTile * kPieces, kValues = NB * kQK * 8;
-  extern __shared__ __attribute__((aligned(16))) uint8_t dynamic[];
-  // [2] buffers of keys and values, then [2][4] whether a granule has a page
-  u32x4* const lds = reinterpret_cast<u32x4*>(dynamic);
-  int* const named = reinterpret_cast<int*>(dynamic + 2 * (kKeys + kValues) * 16);
+  u32x4* const lds = shared.tiles[0];
+  int* const named = shared.named[0];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n = lane & 31, half = lane >> 5;
   int s, h, r0, rows, split;
   Seq q;
-  if (!job_of<R>(a, y, blockIdx.x, places, &s, &h, &r0, &rows, &split, &q)) return;
+  if (!job_of<R>(a, y, block, &s, &h, &r0, &rows, &split, &q)) return;
   const Cache& c = a.cache;
   const UnpackConsts uc = make_unpack_consts();
   const Cap cap(a.softcap);
@@ -192,8 +197,7 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
 
   // Fetching and decoding: wavefront w has granule w % 4 of a tile, the keys in the
   // first four wavefronts, the values in the last four (of four: both).
-  const bool keys_here = wave < 4, values_here = WAVES == 4 || wave >= 4;
-  const int mine = wave & 3;
+  const int mine = wave;
   const int* table = a.batch.tables + static_cast<int64_t>(s) * a.batch.max_pages;
   const int64_t to_values = static_cast<int64_t>(c.per_page) * (288 * NB);
   Bytes<NB> bytes;
@@ -222,7 +226,7 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
     const uint32_t high = __builtin_amdgcn_readlane(at_hi, i), low = __builtin_amdgcn_readlane(at_lo, i);
     fetched_named = high != ~0u;
     const uint8_t* p = head + (fetched_named ? static_cast<uint64_t>(high) << 32 | low : 0);
-    if (keys_here) {
+    {
       const uint32_t* w = reinterpret_cast<const uint32_t*>(p) + lane * NB;
 #pragma unroll
       for (int b = 0; b < NB; ++b) bytes.k[b] = w[b];
@@ -230,7 +234,7 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
 #pragma unroll
       for (int b = 0; b < NB; ++b) bytes.ks[b] = sc[4 * b];
     }
-    if (values_here) {
+    {
       p += to_values;
 #pragma unroll
       for (int i = 0; i < (NB + 3) / 4; ++i) {
@@ -243,23 +247,24 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
       }
     }
   };
-  auto decode = [&](int tile, auto parity) __attribute__((always_inline)) {
-    constexpr int buffer = decltype(parity)::value;
+  auto decode = [&](int tile, int buffer) __attribute__((always_inline)) {
     u32x4* const keys = lds + buffer * (kKeys + kValues);
     u32x4* const values = keys + kKeys;
-    if (keys_here) {
+    {
       const int t = 16 * mine + (lane >> 2), g = lane & 3;
+      int turn = turn_key<NB>(t);
+      if constexpr (NB > 6) tie_after(turn);  // (addresses formed anew: there are too many to keep)
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const Codes k = codes_of(bytes.k[b], uc);
         const half_t d = __builtin_bit_cast(half_t, bytes.ks[b]);
         const half2_t dd = {d, d};
         const half8_t piece = join(k.l02 * dd, k.l13 * dd, k.h02 * dd, k.h13 * dd);
-        keys[t * kPieces + ((4 * b + g) ^ turn_key<NB>(t))] = __builtin_bit_cast(u32x4, piece);
+        keys[t * kPieces + ((4 * b + g) ^ turn)] = __builtin_bit_cast(u32x4, piece);
       }
       if (lane == 0) named[buffer * 4 + mine] = fetched_named;
     }
-    if (values_here) {
+    {
       const int first = tile * kTile + 16 * mine;
       const int from = lo_first - first, to = fetched_named ? hi_last - first : 0;
       const bool whole = from <= 0 && to >= 16;  // unseen places may hold anything
@@ -306,8 +311,10 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
   // The tiles that the wavefront's rows see some of, and those that each sees whole.
   const int some0 = w0 < w1 ? wlo / kTile : t1, some1 = w0 < w1 ? (whi + kTile - 1) / kTile : 0;
   const int whole0 = (wlo_last + kTile - 1) / kTile, whole1 = w1 == w0 + 32 ? whi_first / kTile : 0;
-  auto scores = [&](auto parity) __attribute__((always_inline)) {
-    const u32x4* const keys = lds + decltype(parity)::value * (kKeys + kValues);
+  auto scores = [&](int buffer) __attribute__((always_inline)) {
+    const u32x4* const keys = lds + buffer * (kKeys + kValues);
+    int turn = turn_key<NB>(n);
+    if constexpr (NB > 6) tie_after(turn);  // (addresses formed anew: there are too many to keep)
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -317,17 +324,19 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         const half8_t kf = __builtin_bit_cast(
-            half8_t, keys[(32 * mt + n) * kPieces + ((2 * ks + half) ^ turn_key<NB>(n))]);
+            half8_t, keys[(32 * mt + n) * kPieces + ((2 * ks + half) ^ turn)]);
         x[mt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[ks], x[mt], 0, 0, 0);
       }
   };
-  auto products = [&](auto parity) __attribute__((always_inline)) {
-    const u32x4* const values = lds + decltype(parity)::value * (kKeys + kValues) + kKeys;
+  auto products = [&](int buffer) __attribute__((always_inline)) {
+    const u32x4* const values = lds + buffer * (kKeys + kValues) + kKeys;
+    int turn = turn_value(n);
+    if constexpr (NB > 6) tie_after(turn);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const half8_t vf = __builtin_bit_cast(half8_t, values[(32 * b + n) * 8 + ((2 * k + half) ^ turn_value(n))]);
+        const half8_t vf = __builtin_bit_cast(half8_t, values[(32 * b + n) * 8 + ((2 * k + half) ^ turn)]);
         o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[k], o[b], 0, 0, 0);
       }
   };
@@ -385,12 +394,6 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
       }
     }
   };
-  auto nothing = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p[i][e] = static_cast<half_t>(0.f);
-  };
   // A barrier that waits for this wavefront's LDS accesses alone: fetches stay in flight.
   auto meet = [&]() __attribute__((always_inline)) {
     wait_lgkm0();
@@ -398,60 +401,46 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
     compiler_fence();
   };
 
-  // Two phases a tile, each ended by a barrier: products (the scores of tile t, the
-  // columns of t - 1), then weights of t and the decoding of t + 1.  The second four
-  // wavefronts, one on each SIMD beside one of the first four, run one phase behind, so
-  // that matrix and vector units work at the same time.  In phases of the first four
-  // (the second four one later): tile t's keys and the values of t - 1 are read in 2 t
-  // and 2 t + 1, keys of t + 1 (by the first four) written in 2 t + 1, values of t + 1 (by
-  // the second four) in 2 t + 2: two buffers of each do.
-  const int group = WAVES == 8 ? wave >> 2 : 0;
-  using Even = std::integral_constant<int, 0>;
-  using Odd = std::integral_constant<int, 1>;
+  // A tile: its scores, the decoding of the next tile into the other buffers (which the
+  // barrier behind the tile before has freed), its weights, its products.  The two
+  // workgroups of a compute unit are in different places of this, so that matrix and
+  // vector units work at the same time.
   if (t0 < t1) {
-    for (int i = threadIdx.x; i < kValues; i += WAVES * kWave)  // the values before the first tile
-      lds[kKeys + kValues + kKeys + i] = u32x4{0, 0, 0, 0};
     fetch(t0);
-    decode(t0, Even());
+    decode(t0, 0);
     if (t0 + 1 < t1) fetch(t0 + 1);
     meet();
-    if (group == 1) meet();
-    bool before = false;  // tile t - 1 was seen: p holds its weights, else zeros
-    nothing();
-    auto step = [&](int t, auto mine_, auto other) __attribute__((always_inline)) {
+    auto step = [&](int t, int buffer) __attribute__((always_inline)) {
       const bool seen = t >= some0 && t < some1;
-      there = *reinterpret_cast<const int4*>(named + 4 * decltype(mine_)::value);
-      // (One block, so that reads and products of both run into each other: with no tile
-      // before, its weights are 0.)
-      if (seen || before) {
-        scores(mine_);
-        products(other);
-        feed<8 * NB>();
+      there = *reinterpret_cast<const int4*>(named + 4 * buffer);
+      if (seen) {
+        scores(buffer);
+        feed<4 * NB, kAhead>();
       }
-      meet();
-      if (t + 1 < t1) {  // (first, so that its writes are through before the barrier)
-        decode(t + 1, other);
+      if (t + 1 < t1) {
+        decode(t + 1, buffer ^ 1);
         if (t + 2 < t1) fetch(t + 2);
       }
-      if (seen) weights(t);
-      else nothing();
-      before = seen;
+      if (seen) {
+        weights(t);
+        products(buffer);
+        feed<4 * NB, kAhead>();
+      }
       meet();
     };
-    for (int t = t0; t < t1; t += 2) {
-      step(t, Even(), Odd());
-      if (t + 1 < t1) step(t + 1, Odd(), Even());
+    if constexpr (NB > 6) {
+      for (int t = t0; t < t1; ++t) step(t, (t - t0) & 1);
+    } else {  // (each buffer's addresses are then constants away from the other's)
+      for (int t = t0; t < t1; t += 2) {
+        step(t, 0);
+        if (t + 1 < t1) step(t + 1, 1);
+      }
     }
-    if (before) {
-      if ((t1 - 1 - t0) & 1) products(Odd());
-      else products(Even());
-    }
-    if (WAVES == 8 && group == 0) meet();
   }
 
   l = sum_over_halves(l);
   if (y.splits > 1) {
-    const int64_t at = (blockIdx.x * static_cast<int64_t>(WAVES) + wave);
+    const int64_t at = block * kWaves + wave;
     if (half == 0) *reinterpret_cast<float2*>(y.stats + (at * 32 + n) * 2) = float2{m, l};
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -475,108 +464,78 @@ __global__ __launch_bounds__(WAVES* kWave, WAVES / 4) void attention_many_kernel
   if (a.lse != nullptr && half == 0) a.lse[at] = l > 0.f ? (m - kLift2 + log2f(l)) * kLn2 : -INFINITY;
 }
 
-// The splits' parts of a row tile, in their order; a wavefront takes 32 rows of 32 columns.
-template <int NB, int WAVES>
-__global__ __launch_bounds__(kWave) void attention_splits_kernel(Attention a, Many y, int64_t places) {
-  constexpr int R = 32 * WAVES;
-  const int lane = threadIdx.x, n = lane & 31, half = lane >> 5;
-  const int wave = blockIdx.y / NB, b = blockIdx.y % NB;
+// The splits' parts of a row tile, in their order; a wavefront takes 32 rows (of
+// the first launch's wavefront `wave`) of a block's columns.
+template <int NB>
+__device__ __forceinline__ void attention_splits(const Attention& a, const Many& y, int64_t block, int wave) {
+  constexpr int R = kManyRows;
+  const int lane = threadIdx.x & (kWave - 1), n = lane & 31, half = lane >> 5;
   const int kv = a.cache.kv_heads;
-  const int64_t place = blockIdx.x / kv;  // as the first launch counts them, without its splits
-  const int64_t block0 = place * y.splits * kv + blockIdx.x % kv;
+  const int64_t place = block / kv;  // as the first launch counts them, without its splits
+  const int64_t block0 = place * y.splits * kv + block % kv;
   int s, h, r0, rows, split;
   Seq q;
-  if (!job_of<R>(a, y, block0, places, &s, &h, &r0, &rows, &split, &q)) return;
+  if (!job_of<R>(a, y, block0, &s, &h, &r0, &rows, &split, &q)) return;
   const int row = r0 + 32 * wave + n;
-  float m = -INFINITY, l = 0.f;
-  float4_t v[4];
+  for (int b = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); b < NB; b += kWaves) {
+    float m = -INFINITY, l = 0.f;
+    float4_t v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = float4_t{0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < y.splits; ++i) {
-    const int64_t at = (block0 + static_cast<int64_t>(i) * kv) * WAVES + wave;
-    const float2 st = *reinterpret_cast<const float2*>(y.stats + (at * 32 + n) * 2);
-    const float next = fmaxf(m, st.x), ref = next == -INFINITY ? 0.f : next;
-    const float old = __builtin_amdgcn_exp2f(m - ref), by = __builtin_amdgcn_exp2f(st.x - ref);
-    m = next;
-    l = l * old + st.y * by;
+    for (int i = 0; i < 4; ++i) v[i] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < y.splits; ++i) {
+      const int64_t at = (block0 + static_cast<int64_t>(i) * kv) * kWaves + wave;
+      const float2 st = *reinterpret_cast<const float2*>(y.stats + (at * 32 + n) * 2);
+      const float next = fmaxf(m, st.x), ref = next == -INFINITY ? 0.f : next;
+      const float old = __builtin_amdgcn_exp2f(m - ref), by = __builtin_amdgcn_exp2f(st.x - ref);
+      m = next;
+      l = l * old + st.y * by;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = v[j] * old + y.cols[((at * NB + b) * 4 + j) * kWave + lane] * by;
+      for (int j = 0; j < 4; ++j) v[j] = v[j] * old + y.cols[((at * NB + b) * 4 + j) * kWave + lane] * by;
+    }
+    if (row >= rows) continue;
+    const int token = row / a.group;
+    const int64_t at = static_cast<int64_t>(q.row + token) * a.heads + h * a.group + row - token * a.group;
+    const float inverse = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float out[4] = {v[j][0] * inverse, v[j][1] * inverse, v[j][2] * inverse, v[j][3] * inverse};
+      store4(a.y, a.y_dt, at * (NB * kQK) + b * kQK + 8 * j + 4 * half, out);
+    }
+    if (a.lse != nullptr && half == 0 && b == 0) a.lse[at] = l > 0.f ? (m - kLift2 + log2f(l)) * kLn2 : -INFINITY;
   }
-  if (row >= rows) return;
-  const int token = row / a.group;
-  const int64_t at = static_cast<int64_t>(q.row + token) * a.heads + h * a.group + row - token * a.group;
-  const float inverse = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float out[4] = {v[j][0] * inverse, v[j][1] * inverse, v[j][2] * inverse, v[j][3] * inverse};
-    store4(a.y, a.y_dt, at * (NB * kQK) + b * kQK + 8 * j + 4 * half, out);
-  }
-  if (a.lse != nullptr && half == 0 && b == 0) a.lse[at] = l > 0.f ? (m - kLift2 + log2f(l)) * kLn2 : -INFINITY;
 }
 
-// Heads of more than 128 values leave registers for half as many wavefronts.
-int wavefronts(int dim) { return dim > 128 ? 4 : 8; }
+// ------------------------------------------------------------------ host
 
-int64_t places_of(const Attention& a) {
-  return static_cast<int64_t>(a.batch.tokens) * a.group / (32 * wavefronts(a.cache.dim)) + a.batch.seqs;
+inline int64_t many_places(const Attention& a) {
+  return static_cast<int64_t>(a.batch.tokens) * a.group / kManyRows + a.batch.seqs;
 }
 
-int splits_of(const Attention& a) {
-  const int64_t n = places_of(a) * a.cache.kv_heads, cu = device_cu_count();
-  return n >= cu ? 1 : static_cast<int>(cu / n < 32 ? cu / n : 32);
+// Workgroups that a compute unit holds: heads of more than 128 values take its registers.
+inline int many_per_unit(int dim) { return dim > 128 ? 1 : 2; }
+
+inline int many_splits(const Attention& a) {
+  const int64_t n = many_places(a) * a.cache.kv_heads, room = device_cu_count() * many_per_unit(a.cache.dim);
+  return n >= room ? 1 : static_cast<int>(room / n < 32 ? room / n : 32);
 }
 
-size_t stats_bytes(const Attention& a, int splits) {
-  return static_cast<size_t>(places_of(a)) * a.cache.kv_heads * splits * 32 * wavefronts(a.cache.dim) * 8;
+inline size_t many_stats_bytes(const Attention& a, int splits) {
+  return static_cast<size_t>(many_places(a)) * a.cache.kv_heads * splits * kManyRows * 8;
 }
-
-std::atomic<uint64_t> g_allowed[8][2];
-
-template <int NB, bool BF16>
-hipError_t launch_as(const Attention& a, Many& y, Queue q) {
-  constexpr int kWaves = NB > 4 ? 4 : 8;
-  constexpr int kLds = 2 * (kTile * 4 * NB + NB * kQK * 8) * 16 + 32;
-  Attention args = a;
-  int64_t places = places_of(a);
-  void* argv[] = {&args, &y, &places};
-  const hipError_t e = launch_blocks(reinterpret_cast<const void*>(&attention_many_kernel<NB, kWaves, BF16>),
-                                     places * a.cache.kv_heads * y.splits, kWaves * kWave, argv, kLds, q, 1, 1, kLds,
-                                     &g_allowed[NB - 1][BF16]);
-  if (e != hipSuccess || y.splits == 1) return e;
-  return launch_blocks(reinterpret_cast<const void*>(&attention_splits_kernel<NB, kWaves>),
-                       places * a.cache.kv_heads, kWave, argv, 0, q, kWaves * NB);
-}
-
-template <int NB>
-hipError_t launch_dim(const Attention& a, Many& y, Queue q) {
-  return a.qt == DType::BF16 ? launch_as<NB, true>(a, y, q) : launch_as<NB, false>(a, y, q);
-}
-
-}  // namespace
-
-size_t attention_many_bytes(const Attention& a) {
-  const int splits = splits_of(a);
+inline size_t many_bytes(const Attention& a) {
+  const int splits = many_splits(a);
   if (splits == 1) return 0;
-  return stats_bytes(a, splits) +
-         static_cast<size_t>(places_of(a)) * a.cache.kv_heads * splits * 32 * wavefronts(a.cache.dim) * a.cache.dim * 4;
+  return many_stats_bytes(a, splits) +
+         static_cast<size_t>(many_places(a)) * a.cache.kv_heads * splits * kManyRows * a.cache.dim * 4;
 }
-
-hipError_t launch_attention_many(const Attention& a, int min_rows, void* workspace, Queue q) {
+inline Many make_many(const Attention& a, int min_rows, void* workspace) {
   Many y;
   y.min_rows = min_rows;
-  y.splits = splits_of(a);
+  y.splits = many_splits(a);
+  y.places = many_places(a);
   y.stats = static_cast<float*>(workspace);
-  y.cols = reinterpret_cast<float4_t*>(behind(workspace, stats_bytes(a, y.splits)));
-  switch (a.cache.dim / kQK) {
-    case 1: return launch_dim<1>(a, y, q);
-    case 2: return launch_dim<2>(a, y, q);
-    case 3: return launch_dim<3>(a, y, q);
-    case 4: return launch_dim<4>(a, y, q);
-    case 5: return launch_dim<5>(a, y, q);
-    case 6: return launch_dim<6>(a, y, q);
-    case 7: return launch_dim<7>(a, y, q);
-    default: return launch_dim<8>(a, y, q);
-  }
+  y.cols = reinterpret_cast<float4_t*>(behind(workspace, many_stats_bytes(a, y.splits)));
+  return y;
 }
 
 }  // namespace q4

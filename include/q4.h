@@ -440,7 +440,8 @@ size_t q4_attention_workspace_size(int64_t seqs, int64_t tokens, int64_t heads, 
  *     (single tokens, drafts) take the keys' codes as exact integers and their
  *     scales in fp32; sequences of many rows round the decoded keys to fp16
  *     once.  Decoded values and the weights exp(s_t - m) are rounded to fp16
- *     (with fp16 q and few rows the weights are kept in two fp16 parts).
+ *     (with fp16 q and up to 16 rows, times heads per kv head, a sequence on
+ *     average the weights are kept in two fp16 parts).
  *   - bf16 q are taken as fp16 times a power of two per row and head, as in
  *     q4_linear.
  * Results do not depend on what else runs, but the order of the sums over
