@@ -15,9 +15,18 @@ __global__ __launch_bounds__(kWaves* kWave, per_unit(NB, NT)) void attention_few
 
 template <int NB, int NT>
 __global__ __launch_bounds__(kWaves* kWave) void attention_join_kernel(Attention a, Parts parts) {
-  __shared__ __attribute__((aligned(16))) JoinLds<NB> lds;
-  attention_join<NB, NT>(a, parts, blockIdx.x, blockIdx.y >> 1, blockIdx.y & 1, lds);
+  attention_join<NB, NT>(a, parts, blockIdx.x, blockIdx.y >> 1, blockIdx.y & 1);
 }
+
+template <int NB, int NT>
+__global__ __launch_bounds__(kWaves* kWave) void attention_join_wide_kernel(Attention a, Parts parts) {
+  __shared__ __attribute__((aligned(16))) JoinLds lds;
+  const int y = blockIdx.y;
+  attention_join_wide<NB, NT>(a, parts, blockIdx.x, y / (2 * NB), y / NB % 2, y % NB, lds);
+}
+
+// Notes up to which their parts are spread over workgroups.
+constexpr int kWideNotes = 64;
 
 int workgroups(const Attention& a) {
   return per_unit(a.cache.dim / kQK, few_row_tiles(a)) * device_cu_count();
@@ -31,8 +40,12 @@ hipError_t launch_as(const Attention& a, Few& f, int n, Queue q) {
                                      kWaves * kWave, argv, 0, q);
   if (e != hipSuccess || f.whole) return e;
   void* joined[] = {&args, &f.parts};
-  return launch_blocks(reinterpret_cast<const void*>(&attention_join_kernel<NB, NT>), n, kWaves * kWave, joined, 0, q,
-                       2 * NT);
+  const int notes = f.parts.jobs ? f.parts.jobs : n;
+  if (notes <= kWideNotes)
+    return launch_blocks(reinterpret_cast<const void*>(&attention_join_wide_kernel<NB, NT>), notes, kWaves * kWave,
+                         joined, 0, q, 2 * NT * NB);
+  return launch_blocks(reinterpret_cast<const void*>(&attention_join_kernel<NB, NT>), notes, kWaves * kWave, joined, 0,
+                       q, 2 * NT);
 }
 
 template <int NB>

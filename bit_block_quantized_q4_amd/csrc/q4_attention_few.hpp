@@ -33,12 +33,14 @@ namespace q4 {
 // Parts of rows in the workspace: for each slot NT x 16 rows of (maximum, sum), then
 // their columns as the lanes hold them.
 struct Parts {
-  int* notes = nullptr;     // a note per workgroup
+  // What is noted of the rows whose first part lies with a workgroup as its last one:
+  // {parts (0: there are none), workgroup, sequence, kv head << 16 | first row / 16}; a note
+  // per workgroup, or (jobs) one for each head and 16 NT rows of it.
+  int* notes = nullptr;
+  int jobs = 0;
   float* stats = nullptr;   // [slots][16 NT][2]
   float4_t* cols = nullptr; // [slots][NT][2][NB][64]
 };
-// What a workgroup notes about the rows whose first part is its last one: {parts (0:
-// there are none), sequence, kv head, first row}.
 
 struct Few {
   int max_rows = 0;  // sequences of more rows are left out
@@ -521,110 +523,127 @@ __device__ __forceinline__ void attention_few(const Attention& a, const Few& f, 
           __syncthreads();
         }
       }
-      if (t0 == 0 && !done) {  // this run ends inside the rows' tiles
+      if (t0 == 0 && !f.whole && (!done || f.parts.jobs)) {
+        // done, or this run ends inside the rows' tiles
         const int64_t last = unit + w.tiles - 1;
+        const int count = done ? 0 : static_cast<int>(last / per - block) + 1;
+        const int64_t at = f.parts.jobs ? s * static_cast<int64_t>(w.row_tiles) * c.kv_heads + job : block;
         noted = true;
-        if (threadIdx.x == 0)
-          notes[block] = int4{static_cast<int>(last / per - block) + 1, s, h, r0};
+        if (threadIdx.x == 0) notes[at] = int4{count, block, s, static_cast<int>(static_cast<uint32_t>(h) << 16 | r0 / 16)};
       }
       unit += f.whole ? 1 : t1 - t0;
       ++job;
       t0 = 0;
     }
   }
-  if (!noted && !f.whole && threadIdx.x == 0) notes[block] = int4{0, 0, 0, 0};
+  if (!noted && !f.whole && !f.parts.jobs && threadIdx.x == 0) notes[block] = int4{0, 0, 0, 0};
 }
 
 // Rows whose parts lie with several workgroups: part 0 is the noting workgroup's last
-// (slot 2 w + 1), part i the first one of the i-th behind it (slot 2 (w + i)).  A
-// workgroup takes 16 rows of half the columns (e) of note w; its wavefronts every fourth
-// part, four at a time in flight, and then their sums in order.
+// (slot 2 w + 1), part i the first one of the i-th behind it (slot 2 (w + i)).
+
+// What 16 rows of 16 columns (block blk, half e) have in parts first, first + step, ..,
+// FLIGHT of them at once.
+struct Joined {
+  float top = -INFINITY, sum = 0.f;
+  float4_t v = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(const float2& st, const float4_t& part) {
+    const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.f : next;
+    const float old = __builtin_amdgcn_exp2f(top - ref), by = __builtin_amdgcn_exp2f(st.x - ref);
+    top = next;
+    sum = sum * old + st.y * by;
+    v = v * old + part * by;
+  }
+};
+template <int NB, int NT, int FLIGHT>
+__device__ __forceinline__ Joined join_parts(const Parts& parts, int count, int w, int nt, int e, int blk, int first,
+                                             int step) {
+  const int lane = threadIdx.x & (kWave - 1), m16 = lane & 15;
+  Joined o;
+  for (int i0 = first; i0 < count; i0 += FLIGHT * step) {
+    float2 st[FLIGHT];
+    float4_t part[FLIGHT];
+#pragma unroll
+    for (int j = 0; j < FLIGHT; ++j) {  // (behind the last one: the first again, and not added)
+      const int i = i0 + j * step < count ? i0 + j * step : i0;
+      const int64_t slot = 2 * (static_cast<int64_t>(w) + i) + (i == 0);
+      st[j] = reinterpret_cast<const float2*>(parts.stats)[slot * (16 * NT) + nt * 16 + m16];
+      part[j] = parts.cols[((slot * NT + nt) * 2 + e) * (NB * kWave) + blk * kWave + lane];
+    }
+#pragma unroll
+    for (int j = 0; j < FLIGHT; ++j)
+      if (i0 + j * step < count) o.add(st[j], part[j]);
+  }
+  return o;
+}
 template <int NB>
+__device__ __forceinline__ void store_joined(const Attention& a, const int4& note, const Joined& o, int nt, int e,
+                                             int blk) {
+  const int lane = threadIdx.x & (kWave - 1), m16 = lane & 15, g = lane >> 4;
+  const Seq q = seq_of(a.batch, note.z);
+  const int r = (note.w & 0xFFFF) * 16 + nt * 16 + m16;
+  if (r >= q.rows * a.group) return;
+  const int token = r / a.group, h = static_cast<int>(static_cast<uint32_t>(note.w) >> 16);
+  const int64_t at = static_cast<int64_t>(q.row + token) * a.heads + h * a.group + (r - token * a.group);
+  const float inverse = o.sum > 0.f ? 1.f / o.sum : 0.f;
+  const float out[4] = {o.v[0] * inverse, o.v[1] * inverse, o.v[2] * inverse, o.v[3] * inverse};
+  store4(a.y, a.y_dt, at * (NB * kQK) + blk * kQK + e * 16 + 4 * g, out);
+  if (a.lse != nullptr && g == 0 && e == 0 && blk == 0)
+    a.lse[at] = o.sum > 0.f ? (o.top - kLift + log2f(o.sum)) * kLn2 : -INFINITY;
+}
+
+// Many notes, few parts each: a workgroup takes 16 rows of half the columns (e) of a note,
+// a wavefront every fourth block.
+template <int NB, int NT>
+__device__ __forceinline__ void attention_join(const Attention& a, const Parts& parts, int note_at, int nt, int e) {
+  const int4 note = reinterpret_cast<const int4*>(parts.notes)[note_at];
+  if (note.x == 0) return;
+  for (int blk = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); blk < NB; blk += kWaves)
+    store_joined<NB>(a, note, join_parts<NB, NT, 8>(parts, note.x, note.y, nt, e, blk, 0, 1), nt, e, blk);
+}
+
+// Few notes of many parts: a workgroup takes 16 rows of 16 columns, a wavefront every fourth
+// part.  (For many notes that are mostly empty starting so many workgroups takes 9 us.)
 struct JoinLds {
-  float4_t cols[kWaves][NB][kWave];
+  float4_t cols[kWaves][kWave];
   float2 stats[kWaves][16];
 };
 template <int NB, int NT>
-__device__ __forceinline__ void attention_join(const Attention& a, const Parts& parts, int w, int nt, int e,
-                                               JoinLds<NB>& lds) {
-  constexpr int R = 16 * NT;
-  const int4 note = reinterpret_cast<const int4*>(parts.notes)[w];
+__device__ __forceinline__ void attention_join_wide(const Attention& a, const Parts& parts, int note_at, int nt, int e,
+                                                    int blk, JoinLds& lds) {
+  const int4 note = reinterpret_cast<const int4*>(parts.notes)[note_at];
   if (note.x == 0) return;
-  const int lane = threadIdx.x & (kWave - 1), m16 = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  float top = -INFINITY, sum = 0.f;
-  float4_t v[NB];
-#pragma unroll
-  for (int blk = 0; blk < NB; ++blk) v[blk] = float4_t{0.f, 0.f, 0.f, 0.f};
-  for (int i0 = wave; i0 < note.x; i0 += 4 * kWaves) {
-    float2 st[4];
-    float4_t part[4][NB];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * kWaves < note.x ? i0 + j * kWaves : i0;
-      const int64_t slot = 2 * (static_cast<int64_t>(w) + i) + (i == 0);
-      st[j] = reinterpret_cast<const float2*>(parts.stats)[slot * R + nt * 16 + m16];
-#pragma unroll
-      for (int blk = 0; blk < NB; ++blk)
-        part[j][blk] = parts.cols[((slot * NT + nt) * 2 + e) * (NB * kWave) + blk * kWave + lane];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (i0 + j * kWaves >= note.x) break;
-      const float next = fmaxf(top, st[j].x), ref = next == -INFINITY ? 0.f : next;
-      const float old = __builtin_amdgcn_exp2f(top - ref), by = __builtin_amdgcn_exp2f(st[j].x - ref);
-      top = next;
-      sum = sum * old + st[j].y * by;
-#pragma unroll
-      for (int blk = 0; blk < NB; ++blk) v[blk] = v[blk] * old + part[j][blk] * by;
-    }
-  }
-  if (g == 0) lds.stats[wave][m16] = float2{top, sum};
-#pragma unroll
-  for (int blk = 0; blk < NB; ++blk) lds.cols[wave][blk][lane] = v[blk];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const Joined mine = join_parts<NB, NT, 16>(parts, note.x, note.y, nt, e, blk, wave, kWaves);
+  if (lane < 16) lds.stats[wave][lane] = float2{mine.top, mine.sum};
+  lds.cols[wave][lane] = mine.v;
   __syncthreads();
-  float all = -INFINITY, total = 0.f, by[kWaves];
+  if (wave != 0) return;
+  Joined o;
 #pragma unroll
-  for (int x = 0; x < kWaves; ++x) all = fmaxf(all, lds.stats[x][m16].x);
-  const float ref = all == -INFINITY ? 0.f : all;
-#pragma unroll
-  for (int x = 0; x < kWaves; ++x) {
-    by[x] = __builtin_amdgcn_exp2f(lds.stats[x][m16].x - ref);
-    total = fmaf(lds.stats[x][m16].y, by[x], total);
-  }
-  const Seq q = seq_of(a.batch, note.y);
-  const int rows = q.rows * a.group, r = note.w + nt * 16 + m16;
-  if (r >= rows) return;
-  const int i = r / a.group;
-  const int64_t at = static_cast<int64_t>(q.row + i) * a.heads + note.z * a.group + (r - i * a.group);
-  const float inverse = total > 0.f ? 1.f / total : 0.f;
-  for (int blk = wave; blk < NB; blk += kWaves) {
-    float4_t o = lds.cols[0][blk][lane] * by[0];
-#pragma unroll
-    for (int x = 1; x < kWaves; ++x) o += lds.cols[x][blk][lane] * by[x];
-    const float out[4] = {o[0] * inverse, o[1] * inverse, o[2] * inverse, o[3] * inverse};
-    store4(a.y, a.y_dt, at * (NB * kQK) + blk * kQK + e * 16 + 4 * g, out);
-  }
-  if (a.lse != nullptr && g == 0 && e == 0 && wave == 0)
-    a.lse[at] = total > 0.f ? (all - kLift + log2f(total)) * kLn2 : -INFINITY;
+  for (int x = 0; x < kWaves; ++x) o.add(lds.stats[x][lane & 15], lds.cols[x][lane]);
+  store_joined<NB>(a, note, o, nt, e, blk);
 }
 
 // ------------------------------------------------------------------ host
 
-// Rows per product: 16 rows, or 32 where the sequences have more on average (and their
-// sums fit the registers).
+// Rows per product: 16 rows, or 32 where the sequences have more on average and registers
+// hold their sums: of up to 192 columns, and beside sequences of many rows (which take
+// three workgroups a compute unit for up to 64) of more than 64.
 inline int few_row_tiles(const Attention& a) {
   const int64_t rows = static_cast<int64_t>(a.batch.tokens) * a.group;
-  return rows > static_cast<int64_t>(a.batch.seqs) * 16 && a.cache.dim <= 192 ? 2 : 1;
+  const bool room = a.cache.dim <= 192 && (a.batch.offsets == nullptr || a.cache.dim > 64);
+  return room && rows > static_cast<int64_t>(a.batch.seqs) * 16 ? 2 : 1;
 }
 
 // Whether a head's tiles are few enough for one workgroup: as many as its wavefronts take
-// in four turns.  (One token of 1000 positions: 12.3 us cut and joined, WHOLE_US so.)
+// in two turns.  (A turn more is 1.6 us, the second launch 4: one token of 1000 positions,
+// four turns, 12.3 us cut and joined, 13.6 whole.)
 inline bool few_whole(const Attention& a) {
   int64_t most = a.batch.max_length;
   const int64_t within = static_cast<int64_t>(a.window) + 32 + kTile;  // of 32 rows, from any place of a tile on
   if (a.window > 0 && within < most) most = within;
-  return most <= 16 * kTile;
+  return most <= 8 * kTile;
 }
 
 // The parts of n workgroups in the workspace.
@@ -634,11 +653,17 @@ inline size_t few_bytes(const Attention& a, int n) {
   const int nt = few_row_tiles(a);
   return notes_bytes(n) + few_stats_bytes(n, nt) + static_cast<size_t>(n) * 2 * nt * 16 * a.cache.dim * 4;
 }
+// (notes: as many as there are workgroups, also where they go by jobs: those are no more.)
 inline Few make_few(const Attention& a, int n, int max_rows, void* workspace) {
   Few f;
   f.max_rows = max_rows;
   f.whole = few_whole(a);
   f.least = f.whole ? 1 : kWaves;
+  if (a.batch.offsets == nullptr) {  // all sequences have the rows of one token
+    const int rows = 16 * few_row_tiles(a);
+    const int64_t jobs = static_cast<int64_t>(a.batch.seqs) * a.cache.kv_heads * ((a.group + rows - 1) / rows);
+    f.parts.jobs = jobs <= n ? static_cast<int>(jobs) : 0;
+  }
   f.parts.notes = static_cast<int*>(workspace);
   f.parts.stats = reinterpret_cast<float*>(behind(workspace, notes_bytes(n)));
   f.parts.cols = reinterpret_cast<float4_t*>(behind(workspace, notes_bytes(n) + few_stats_bytes(n, few_row_tiles(a))));

@@ -511,8 +511,8 @@ inline int64_t many_places(const Attention& a) {
   return static_cast<int64_t>(a.batch.tokens) * a.group / kManyRows + a.batch.seqs;
 }
 
-// Workgroups that a compute unit holds: heads of more than 128 values take its registers.
-inline int many_per_unit(int dim) { return dim > 128 ? 1 : 2; }
+// Workgroups that a compute unit holds, by their registers.
+inline int many_per_unit(int dim) { return dim > 128 ? 1 : dim > 64 ? 2 : 3; }
 
 inline int many_splits(const Attention& a) {
   const int64_t n = many_places(a) * a.cache.kv_heads, room = device_cu_count() * many_per_unit(a.cache.dim);

@@ -18,7 +18,7 @@ union Lds {
 };
 
 template <int NB, int NT, bool BF16>
-__global__ __launch_bounds__(kWaves* kWave, NB > 4 ? 1 : 2) void attention_mixed_kernel(Attention a, Few f, Many y,
+__global__ __launch_bounds__(kWaves* kWave, NB > 4 ? 1 : NB > 2 ? 2 : 3) void attention_mixed_kernel(Attention a, Few f, Many y,
                                                                                           int few) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dynamic[];
   Lds<NB, NT>& lds = *reinterpret_cast<Lds<NB, NT>*>(dynamic);
@@ -28,9 +28,8 @@ __global__ __launch_bounds__(kWaves* kWave, NB > 4 ? 1 : 2) void attention_mixed
 
 template <int NB, int NT>
 __global__ __launch_bounds__(kWaves* kWave) void attention_finish_kernel(Attention a, Parts parts, Many y, int joins) {
-  __shared__ __attribute__((aligned(16))) JoinLds<NB> lds;
   const int block = blockIdx.x;
-  if (block < joins) attention_join<NB, NT>(a, parts, block / (2 * NT), block / 2 % NT, block & 1, lds);
+  if (block < joins) attention_join<NB, NT>(a, parts, block / (2 * NT), block / 2 % NT, block & 1);
   else attention_splits<NB>(a, y, (block - joins) / kWaves, (block - joins) % kWaves);
 }
 
@@ -58,7 +57,7 @@ hipError_t launch_as(const Attention& a, Few& f, Many& y, int few, Queue q) {
 template <int NB>
 hipError_t launch_dim(const Attention& a, Few& f, Many& y, int few, Queue q) {
   const bool bf = a.qt == DType::BF16;
-  if constexpr (NB <= 6) {
+  if constexpr (NB > 2 && NB <= 6) {
     if (few_row_tiles(a) == 2)
       return bf ? launch_as<NB, 2, true>(a, f, y, few, q) : launch_as<NB, 2, false>(a, f, y, few, q);
   }
