@@ -13,10 +13,7 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Finite, of at most fp16's largest magnitude: NaN counts as 0.
-__device__ __forceinline__ float storable(float v) {
-  return v != v ? 0.f : fminf(fmaxf(v, -65504.f), 65504.f);
-}
+using u16x2 = uint16_t __attribute__((ext_vector_type(2)));
 
 // What a workgroup of the granule grid takes: positions [from, to) of granule g of
 // sequence s, the rows from `row` on.  False: nothing.
@@ -46,34 +43,72 @@ __device__ __forceinline__ bool granule_of(const Batch& b, int64_t place, Granul
 
 // ------------------------------------------------------------------ writing
 
-// Sixteen consecutive elements of a row, as fp32 (exact), limited to what is stored.
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
-  constexpr int kPieces = sizeof(T);  // of 16 bytes
-  u32x4 w[kPieces];
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      v[i] = __builtin_bit_cast(float, static_cast<uint32_t>(w[i / 4][i % 4]));
-    } else {
-      const uint32_t two = w[i / 8][i / 2 % 4];
-      const uint32_t bits = i % 2 ? two >> 16 : two & 0xFFFFu;
-      if constexpr (std::is_same<T, half_t>::value) v[i] = half_bits_to_float(static_cast<uint16_t>(bits));
-      else v[i] = bf16_bits_to_float(bits);
-    }
-    v[i] = storable(v[i]);
-  }
+// Finite, of at most fp16's largest magnitude: NaN counts as 0.
+__device__ __forceinline__ float storable(float v) {
+  return v != v ? 0.f : fminf(fmaxf(v, -65504.f), 65504.f);
 }
+
+// Sixteen consecutive elements of a row as they lie there.
+template <typename T>
+struct Raw {
+  u32x4 w[sizeof(T)];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
+  }
+  // As fp32 (exact), limited to what is stored.  Magnitudes compare as their bits do:
+  // rarely is one above the limit (NaN, infinities), and only then is each looked at.
+  __device__ __forceinline__ void values(float (&v)[16]) const {
+    constexpr bool kWide = sizeof(T) == 4, kHalf = std::is_same<T, half_t>::value;
+    uint32_t top = 0;
+    if constexpr (kWide) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t m = w[i / 4][i % 4] & 0x7FFFFFFFu;
+        top = m > top ? m : top;
+      }
+    } else {
+      u16x2 most = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const u16x2 m = __builtin_bit_cast(u16x2, w[i / 4][i % 4] & 0x7FFF7FFFu);
+        most = __builtin_elementwise_max(most, m);
+      }
+      top = most.x > most.y ? most.x : most.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (kWide) {
+        v[i] = __builtin_bit_cast(float, static_cast<uint32_t>(w[i / 4][i % 4]));
+      } else {
+        const uint32_t two = w[i / 8][i / 2 % 4];
+        if constexpr (kHalf) v[i] = half_bits_to_float(static_cast<uint16_t>(i % 2 ? two >> 16 : two));
+        else v[i] = __builtin_bit_cast(float, i % 2 ? two & 0xFFFF0000u : two << 16);
+      }
+    }
+    constexpr uint32_t kLimit = kWide ? 0x477FE000u : kHalf ? 0x7BFFu : 0x477Fu;  // (65504; bf16 65280)
+    if (top > kLimit) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = storable(v[i]);
+    }
+  }
+};
 
 // The Q4_0 rule on two lanes, 0 and 1 of a pair holding elements 0 .. 15 and 16 .. 31.
 // Returns the scale; words[0 .. 1] are this lane's code bytes, 0 .. 7 or 8 .. 15.
 //   m: the larger of max and -min; where they are equal the one that comes first.
-//   code: trunc(x / d + 8.5).  t = fma(x, 1 / d, 8.5) differs from the rule's t, two
-//   roundings, by less than 2^-17 (|x / d| <= 8.01; the reciprocal is good to 2^-23),
-//   so only a t within 2^-16 of an integer can truncate differently: those blocks redo
-//   the rule's own division.
+//   code: trunc(x / d + 8.5).  u = fma(x, 1 / d, 8.5) differs from the rule's t, two
+//   roundings, by less than 2^-17 (|x / d| < 16, and a subnormal d is needed for more than
+//   8.01; the reciprocal is good to 2^-22).  Below, 2^-16 is added to u.
+//   EXACT (x of 16 bits): t is an integer or more than 2^-13 from one.  For x / d to be
+//   near k + 1/2, |x| is about d / 2 or more; x and d (k + 1/2) are multiples of 2^-12 d or
+//   of larger powers of two, as both have at most 11 bits (15 with the factor 2 k + 1,
+//   whose unit is d's, halved).  So u truncates as t does: an integer t to itself.
+//   (Such t are common: with bf16, 2 elements of 1000.)
+//   Otherwise a t within 2^-16 of an integer can truncate differently; those are the ones
+//   where the fraction is below 2^-15 (u's own rounding, 2^-20, fits between).  Their blocks
+//   redo the rule's own division, and any other truncates alike with what was added.
+template <bool EXACT>
 __device__ __forceinline__ half_t quantize_pair(int upper, const float (&v)[16], uint32_t (&words)[2]) {
   float most = v[0], least = v[0];
 #pragma unroll
@@ -108,12 +143,12 @@ __device__ __forceinline__ half_t quantize_pair(int upper, const float (&v)[16],
     uint32_t q[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float u = fmaf(v[i], r, 8.5f);
-      near = fminf(near, fabsf(u - __builtin_rintf(u)));
+      const float u = fmaf(v[i], r, 8.5f + 0x1p-16f);
+      if constexpr (!EXACT) near = fminf(near, __builtin_amdgcn_fractf(u));
       const int c = static_cast<int>(u);
       q[i] = static_cast<uint32_t>(c < 0 ? 0 : c > 15 ? 15 : c);
     }
-    if (near < 0x1p-16f) {
+    if (!EXACT && near < 0x1p-15f) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float e = v[i] / D;
@@ -136,70 +171,94 @@ __device__ __forceinline__ half_t quantize_pair(int upper, const float (&v)[16],
   return dh;
 }
 
+// Pieces of 16 bytes in a granule's image: eight, then one left free, so that the values'
+// bytes of a position, sixteen apart, lie in other banks for each block and half.
+__device__ __forceinline__ int piece_at(int i) { return 16 * (i + (i >> 3)); }
+__device__ __forceinline__ int byte_at(int i) { return i + 16 * (i >> 7); }
+constexpr int kImage = 16 * (144 + 144 / 8);
+
 // Two lanes to a block of 32 values.  Code bytes and scales are put together as the
 // granule's image in LDS; a whole granule then leaves in 16-byte pieces, a part of one
-// as what belongs to its positions: words of a key, single bytes of values.
+// as what belongs to its positions: words of a key, single bytes of values.  A workgroup
+// takes `per` kv heads in turn, the next one's rows on their way while this one's are
+// worked on, images by turns.
 template <typename T, int THREADS>
 __global__ __launch_bounds__(THREADS) void cache_write_kernel(Cache c, Batch b, const T* __restrict__ k,
                                                               int64_t k_stride, const T* __restrict__ v,
-                                                              int64_t v_stride) {
-  __shared__ __attribute__((aligned(16))) uint8_t image[2][9 * 256];
-  const int64_t place = blockIdx.x / c.kv_heads;
-  const int h = static_cast<int>(blockIdx.x - place * c.kv_heads);
+                                                              int64_t v_stride, int per, int chunks) {
+  __shared__ __attribute__((aligned(16))) uint8_t images[2][2][kImage];
+  const int64_t place = blockIdx.x / chunks;
+  const int h0 = static_cast<int>(blockIdx.x - place * chunks) * per;
+  const int heads = c.kv_heads - h0 < per ? c.kv_heads - h0 : per;
   Granule gr;
   if (!granule_of(b, place, &gr)) return;
-  uint8_t* const keys = granule_at(c, b, gr.s, gr.g, h);
+  uint8_t* keys = granule_at(c, b, gr.s, gr.g, h0);
   if (keys == nullptr) return;
   const int64_t to_values = static_cast<int64_t>(c.per_page) * (9 * c.dim);
   const int nb = c.dim / kQK, upper = threadIdx.x & 1;
   const int n = gr.to - gr.from, tasks = 2 * n * nb;
-  for (int t = threadIdx.x >> 1; t < tasks; t += THREADS / 2) {
+  const auto row_of = [&](int t, int h) __attribute__((always_inline)) {
     const bool value = t >= n * nb;
-    const int u = value ? t - n * nb : t;
-    const int i = u / nb, blk = u - i * nb, at = gr.from + i;
+    const int u = value ? t - n * nb : t, i = u / nb, blk = u - i * nb;
     const int64_t row = gr.row + i;
-    float x[16];
-    load16((value ? v + row * v_stride : k + row * k_stride) + h * c.dim + blk * kQK + 16 * upper, x);
-    uint32_t words[2];
-    const uint16_t bits = __builtin_bit_cast(uint16_t, quantize_pair(upper, x, words));
-    uint8_t* const g = image[value];
-    uint16_t* const scales = reinterpret_cast<uint16_t*>(g + 8 * c.dim);
-    if (value) {
+    return (value ? v + row * v_stride : k + row * k_stride) + h * c.dim + blk * kQK + 16 * upper;
+  };
+  const int mine = threadIdx.x >> 1;
+  const T* const first = mine < tasks ? row_of(mine, h0) : k;
+  Raw<T> raw = {};
+  if (mine < tasks) raw.load(first);
+  for (int h = 0; h < heads; ++h, keys += c.head_bytes) {
+    uint8_t(&image)[2][kImage] = images[h & 1];
+    for (int t = mine; t < tasks; t += THREADS / 2) {
+      if (t != mine) raw.load(row_of(t, h0 + h));
+      float x[16];
+      raw.values(x);
+      if (t + THREADS / 2 >= tasks && h + 1 < heads) raw.load(first + (h + 1) * c.dim);
+      const bool value = t >= n * nb;
+      const int u = value ? t - n * nb : t, i = u / nb, blk = u - i * nb, at = gr.from + i;
+      uint32_t words[2];
+      const uint16_t bits = __builtin_bit_cast(uint16_t, quantize_pair<sizeof(T) == 2>(upper, x, words));
+      uint8_t* const g = image[value];
+      int scale;  // its byte
+      if (value) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        g[(blk * 16 + 8 * upper + e) * 16 + at] = static_cast<uint8_t>(words[e >> 2] >> (8 * (e & 3)));
-      const int quarter = at & 3;
-      if (upper == 0) scales[blk * 16 + (at & ~3) + (quarter & 1) * 2 + (quarter >> 1)] = bits;
-    } else {
+        for (int e = 0; e < 8; ++e)
+          g[piece_at(blk * 16 + 8 * upper) + 16 * e + at] = static_cast<uint8_t>(words[e >> 2] >> (8 * (e & 3)));
+        const int quarter = at & 3;
+        scale = 8 * c.dim + 2 * (blk * 16 + (at & ~3) + (quarter & 1) * 2 + (quarter >> 1));
+      } else {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        *reinterpret_cast<uint32_t*>(g + at * (c.dim / 2) + ((2 * upper + e) * nb + blk) * 4) = words[e];
-      if (upper == 0) scales[((at >> 2) * nb + blk) * 4 + (at & 3)] = bits;
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<uint32_t*>(g + byte_at(at * (c.dim / 2) + ((2 * upper + e) * nb + blk) * 4)) = words[e];
+        scale = 8 * c.dim + 2 * (((at >> 2) * nb + blk) * 4 + (at & 3));
+      }
+      if (upper == 0) *reinterpret_cast<uint16_t*>(g + byte_at(scale)) = bits;
     }
-  }
-  __syncthreads();
-  if (n == kGranule) {
-    const int pieces = 9 * c.dim / 16;
-    for (int i = threadIdx.x; i < 2 * pieces; i += THREADS) {
-      const int w = i >= pieces, j = i - w * pieces;
-      *reinterpret_cast<u32x4*>(keys + w * to_values + 16 * j) = *reinterpret_cast<const u32x4*>(image[w] + 16 * j);
+    __syncthreads();  // (an image is written again only after the next one's barrier)
+    if (n == kGranule) {
+      const int pieces = 9 * c.dim / 16;
+      for (int i = threadIdx.x; i < 2 * pieces; i += THREADS) {
+        const int w = i >= pieces, j = i - w * pieces;
+        *reinterpret_cast<u32x4*>(keys + w * to_values + 16 * j) =
+            *reinterpret_cast<const u32x4*>(image[w] + piece_at(j));
+      }
+      continue;
     }
-    return;
-  }
-  const int words = n * nb * 4;  // a key's code words lie together
-  for (int i = threadIdx.x; i < words; i += THREADS) {
-    const int at = gr.from * nb * 4 + i;
-    reinterpret_cast<uint32_t*>(keys)[at] = reinterpret_cast<const uint32_t*>(image[0])[at];
-  }
-  for (int i = threadIdx.x; i < n * nb * 16; i += THREADS) {
-    const int byte = i / n, at = byte * 16 + gr.from + i - byte * n;
-    keys[to_values + at] = image[1][at];
-  }
-  for (int i = threadIdx.x; i < 2 * n * nb; i += THREADS) {
-    const int w = i >= n * nb, u = i - w * n * nb, t = gr.from + u / nb, blk = u % nb, quarter = t & 3;
-    const int at = w ? blk * 16 + (t & ~3) + (quarter & 1) * 2 + (quarter >> 1) : ((t >> 2) * nb + blk) * 4 + quarter;
-    reinterpret_cast<uint16_t*>(keys + w * to_values + 8 * c.dim)[at] =
-        reinterpret_cast<const uint16_t*>(image[w] + 8 * c.dim)[at];
+    const int words = n * nb * 4;  // a key's code words lie together
+    for (int i = threadIdx.x; i < words; i += THREADS) {
+      const int at = gr.from * nb * 4 + i;
+      reinterpret_cast<uint32_t*>(keys)[at] = *reinterpret_cast<const uint32_t*>(image[0] + byte_at(4 * at));
+    }
+    for (int i = threadIdx.x; i < n * nb * 16; i += THREADS) {
+      const int byte = i / n, at = byte * 16 + gr.from + i - byte * n;
+      keys[to_values + at] = image[1][byte_at(at)];
+    }
+    for (int i = threadIdx.x; i < 2 * n * nb; i += THREADS) {
+      const int w = i >= n * nb, u = i - w * n * nb, t = gr.from + u / nb, blk = u % nb, quarter = t & 3;
+      const int at = 8 * c.dim + 2 * (w ? blk * 16 + (t & ~3) + (quarter & 1) * 2 + (quarter >> 1)
+                                        : ((t >> 2) * nb + blk) * 4 + quarter);
+      *reinterpret_cast<uint16_t*>(keys + w * to_values + at) = *reinterpret_cast<const uint16_t*>(image[w] + byte_at(at));
+    }
   }
 }
 
@@ -305,17 +364,26 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(Cache c, Batch b, 
   }
 }
 
+// Kv heads that a workgroup takes in turn: up to eight where there are plenty of granules.
+int heads_in_turn(const Cache& c, int64_t places) {
+  const int64_t plenty = places * c.kv_heads / (8 * static_cast<int64_t>(device_cu_count()));
+  const int per = plenty < 1 ? 1 : plenty < 8 ? static_cast<int>(plenty) : 8;
+  return per < c.kv_heads ? per : c.kv_heads;
+}
+
 template <typename T>
 hipError_t write_as(const Cache& c, const Batch& b, const void* k, int64_t k_stride, const void* v,
                     int64_t v_stride, Queue q) {
   Cache ca = c;
   Batch ba = b;
   const T *kp = static_cast<const T*>(k), *vp = static_cast<const T*>(v);
-  void* argv[] = {&ca, &ba, &kp, &k_stride, &vp, &v_stride};
-  const int64_t n = granule_places(b) * c.kv_heads;
-  if (b.offsets == nullptr)  // one position each: a wavefront has lanes for it
-    return launch_blocks(reinterpret_cast<const void*>(&cache_write_kernel<T, kWave>), n, kWave, argv, 0, q);
-  return launch_blocks(reinterpret_cast<const void*>(&cache_write_kernel<T, kThreads>), n, kThreads, argv, 0, q);
+  const int64_t places = granule_places(b);
+  // One position each: a wavefront has lanes for a head's, and a head is soon done.
+  const bool one = b.offsets == nullptr;
+  int per = one ? 1 : heads_in_turn(c, places), chunks = (c.kv_heads + per - 1) / per;
+  void* argv[] = {&ca, &ba, &kp, &k_stride, &vp, &v_stride, &per, &chunks};
+  if (one) return launch_blocks(reinterpret_cast<const void*>(&cache_write_kernel<T, kWave>), places * chunks, kWave, argv, 0, q);
+  return launch_blocks(reinterpret_cast<const void*>(&cache_write_kernel<T, kThreads>), places * chunks, kThreads, argv, 0, q);
 }
 
 template <typename T>
@@ -323,10 +391,8 @@ hipError_t read_as(const Cache& c, const Batch& b, void* k, void* v, Queue q) {
   Cache ca = c;
   Batch ba = b;
   T *kp = static_cast<T*>(k), *vp = static_cast<T*>(v);
-  // Heads that a workgroup takes in turn: eight where there are plenty of granules.
-  const int64_t places = granule_places(b), plenty = places * c.kv_heads / (8 * static_cast<int64_t>(device_cu_count()));
-  int per = plenty < 1 ? 1 : plenty < 8 ? static_cast<int>(plenty) : 8;
-  if (per > c.kv_heads) per = c.kv_heads;
+  const int64_t places = granule_places(b);
+  int per = heads_in_turn(c, places);
   int chunks = (c.kv_heads + per - 1) / per;
   void* argv[] = {&ca, &ba, &kp, &vp, &per, &chunks};
   return launch_blocks(reinterpret_cast<const void*>(&cache_read_kernel<T>), places * chunks, kThreads, argv, 0, q);
