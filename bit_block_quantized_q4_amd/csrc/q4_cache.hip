@@ -1,8 +1,13 @@
 // Writing and reading the paged Q4_0 cache of keys and values.
 //
 // A workgroup takes one granule (sixteen positions) of one sequence and kv head,
-// keys and values.  Grids are sized from the numbers of rows and sequences alone
-// (granule_places); what a place holds is found on the device.
+// keys and values, of some kv heads in turn.  Grids are sized from the numbers of rows and
+// sequences alone (granule_places); what a place holds is found on the device.
+//
+// Both only move bytes: reading 400 MB of cache to 1.4 GB of fp16 takes 426 us, 4.3 TB/s
+// (a large copy: 4.65).  Writing 37 MB from 131 MB of bf16 takes 54 us, 3.1 TB/s: the 16
+// codes of a lane are some 300 vector instructions, which at four wavefronts to a SIMD take
+// as long as its bytes do.  Reading that back takes 36 us, 4.7 TB/s.
 #include <type_traits>
 
 #include "q4_cache.hpp"
@@ -364,9 +369,12 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(Cache c, Batch b, 
   }
 }
 
-// Kv heads that a workgroup takes in turn: up to eight where there are plenty of granules.
+// Kv heads that a workgroup takes in turn, so that the search for its place is made once:
+// up to eight, of sixteen workgroups a compute unit or more.  (One, two, four, eight:
+// reading 400 MB of cache to fp16 565, 502, 437, 426 us; 37 MB of it to bf16 46, 39, 36
+// and 41 us, as so few workgroups do not come out even; writing those 68, 55, 53, 53.)
 int heads_in_turn(const Cache& c, int64_t places) {
-  const int64_t plenty = places * c.kv_heads / (8 * static_cast<int64_t>(device_cu_count()));
+  const int64_t plenty = places * c.kv_heads / (16 * static_cast<int64_t>(device_cu_count()));
   const int per = plenty < 1 ? 1 : plenty < 8 ? static_cast<int>(plenty) : 8;
   return per < c.kv_heads ? per : c.kv_heads;
 }
