@@ -941,8 +941,8 @@ def q4_attention(q, cache, tables, lengths, offsets=None, scale=None, causal=Tru
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
     if int(window) < 0:
         raise ValueError(f"window must be 0 (none) or more; got {window}")
-    options = AttentionOptions(c.head_dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window),
-                               float(softcap))
+    options = AttentionOptions(c.head_dim ** -0.5 if scale is None else float(scale), 1 if causal else 0,
+                               min(int(window), 2 ** 62), float(softcap))
     qd = _dtype_code(q)
     L = lib()
     workspace, wptr, wbytes = _workspace(
