@@ -38,8 +38,8 @@ struct Many {
   float4_t* cols = nullptr; // [workgroups][wavefronts][NB][4][64]
 };
 
-// Row tiles of R rows, as places of a grid: sequence s has the places from
-// row_place(s) on, more than it has tiles.
+// Row tiles of R rows, as places of a grid: sequence s has the places from row_place(s)
+// on, at least as many as it has tiles; without offsets exactly as many.
 __device__ __forceinline__ int64_t row_place(const Batch& b, int group, int rows, int s) {
   return static_cast<int64_t>(offset_of(b, s)) * group / rows + s;
 }
@@ -54,12 +54,14 @@ __device__ __forceinline__ bool job_of(const Attention& a, const Many& y, int64_
   at /= kv;
   *split = static_cast<int>(at % y.splits);
   const int64_t place = y.places - 1 - at / y.splits;
-  *s = a.batch.offsets == nullptr ? static_cast<int>(place) : last_not_above(a.batch.seqs, place, [&](int i) {
+  const bool alike = a.batch.offsets == nullptr;  // one token each
+  const int per = (a.group + R - 1) / R;
+  *s = alike ? static_cast<int>(place / per) : last_not_above(a.batch.seqs, place, [&](int i) {
     return row_place(a.batch, a.group, R, i);
   });
   *q = seq_of(a.batch, *s);
   const int64_t n = static_cast<int64_t>(q->rows) * a.group;
-  const int64_t first = a.batch.offsets == nullptr ? 0 : (place - row_place(a.batch, a.group, R, *s)) * R;
+  const int64_t first = (place - (alike ? static_cast<int64_t>(*s) * per : row_place(a.batch, a.group, R, *s))) * R;
   if (n < y.min_rows || first < 0 || first >= n) return false;
   *r0 = static_cast<int>(first);
   *rows = static_cast<int>(n);
