@@ -5,10 +5,10 @@
 //
 // with keys and values rounded to fp16 as they are decoded, once for all the rows of a
 // workgroup.  A kv head's heads and a sequence's rows together are the rows; a
-// wavefront takes 32 of them, a workgroup as many as it has wavefronts, and walks over
-// the positions in tiles of 64.  Each tile is decoded into one of two LDS buffers by
-// all wavefronts (wavefront w the granule w % 4) while the other is multiplied; the
-// next tile's bytes are on their way in registers meanwhile.
+// wavefront takes 32 of them, a workgroup 128, and walks over the positions in tiles of
+// 64.  Each tile is decoded into one of two LDS buffers, a granule by each wavefront,
+// while the other is multiplied; the next tile's bytes are on their way in registers
+// meanwhile.
 //
 // LDS holds 16-byte pieces, the operands of v_mfma_f32_32x32x16_f16 as they are read:
 //   K  position t, piece 4 b + g: elements 4 g + {0, 2, 1, 3, 16, 18, 17, 19} of block
@@ -18,8 +18,22 @@
 //      of the second product where they are
 // The piece number is exclusive-ored with the row's so that rows lie in other banks.
 //
-// Where there are fewer workgroups than compute units the positions are split as well,
-// and the parts joined in a second launch.
+// Where there are fewer workgroups than compute units hold the positions are split as
+// well, and the parts joined in a second launch.
+//
+// Bound by issuing vector instructions (taking codes apart, exp, the maximum) beside the
+// matrix products: of 730 us for a prompt of 8000 (40 heads of 128 on 8, bf16) the products
+// alone take 436, the softmax alone 256; without decoding it is 627, without the softmax
+// 575.  That is 890 TFLOP/s of products, 71% of a large library product's rate.  So
+// what counts is that other wavefronts have products ready: two workgroups share a compute
+// unit (three for heads of up to 64), each SIMD with two wavefronts that no barrier ties to
+// one another.  Rows by wavefronts, for that prompt, 512 rows behind 32488 positions, and
+// six ragged prompts with heads of 64 (us):
+//   32 x 4, two workgroups a unit    730  411   80
+//   32 x 8, opposite halves' phases  735  505  127
+//   32 x 8                           774  553  121
+//   16 x 8                           774  436   81
+//   16 x 16, opposite phases         790  603  117
 #pragma once
 
 #include "q4_attention.hpp"
@@ -197,8 +211,7 @@ __device__ __forceinline__ void attention_many(const Attention& a, const Many& y
     }
   }
 
-  // Fetching and decoding: wavefront w has granule w % 4 of a tile, the keys in the
-  // first four wavefronts, the values in the last four (of four: both).
+  // Fetching and decoding: a wavefront has a granule of a tile, keys and values.
   const int mine = wave;
   const int* table = a.batch.tables + static_cast<int64_t>(s) * a.batch.max_pages;
   const int64_t to_values = static_cast<int64_t>(c.per_page) * (288 * NB);

@@ -348,8 +348,8 @@ q4_status q4_moe(const void *x, int x_dtype, const void *logits, int logits_dtyp
  * The cache holds head_dim values of keys and of values for every position and
  * kv head, quantised by the rule at the top of this header, 32 values along
  * head_dim to a block, after these steps: a value is limited to +-65504 (an
- * infinity counts as that, NaN as 0), so every decoded value is a finite fp16
- * range number.  It is [pages][kv_heads][2][page_size / 16] granules of 9
+ * infinity counts as that, NaN as 0), so every decoded value is finite and within
+ * fp16's range.  It is [pages][kv_heads][2][page_size / 16] granules of 9
  * head_dim bytes ([2]: keys, values), sixteen positions each: 8 head_dim code
  * bytes, then head_dim / 2 fp16 scales.  With blocks = head_dim / 32, position
  * t = 0 .. 15 of the granule and code byte i = 0 .. 15 of a block b:
