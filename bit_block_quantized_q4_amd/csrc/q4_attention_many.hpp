@@ -18,6 +18,14 @@
 //      of the second product where they are
 // The piece number is exclusive-ored with the row's so that rows lie in other banks.
 //
+// Three things are rounded to fp16, each once: a decoded key, a weight and a decoded value
+// (a code times its scale has up to 15 bits).  For fp16 outputs over random keys and values
+// that makes 4.0e-4 of y (2-norms), where rounding y alone makes 2.1e-4; bf16 outputs hide
+// it (1.7e-3 either way).  Exact codes with the scales as fp32 factors of each block's
+// scores, and weights in two parts, bring it to 2.7e-4, but for 128 more vector
+// instructions and half as many products again a tile: 512 rows behind 32488 positions 623
+// us, not 411.  (q of 32 bits goes another way, with no rounding.)
+//
 // Where there are fewer workgroups than compute units hold the positions are split as
 // well, and the parts joined in a second launch.
 //
