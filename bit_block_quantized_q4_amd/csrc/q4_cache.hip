@@ -4,10 +4,10 @@
 // keys and values, of some kv heads in turn.  Grids are sized from the numbers of rows and
 // sequences alone (granule_places); what a place holds is found on the device.
 //
-// Both only move bytes: reading 400 MB of cache to 1.4 GB of fp16 takes 426 us, 4.3 TB/s
-// (a large copy: 4.65).  Writing 37 MB from 131 MB of bf16 takes 54 us, 3.1 TB/s: the 16
+// Both only move bytes: reading 401 MB of cache to 1.4 GB of fp16 takes 426 us, 4.3 TB/s
+// (a large copy: 4.65).  Writing 44 MB from 156 MB of bf16 takes 54 us, 3.7 TB/s: the 16
 // codes of a lane are some 300 vector instructions, which at four wavefronts to a SIMD take
-// as long as its bytes do.  Reading that back takes 36 us, 4.7 TB/s.
+// as long as its bytes do.  Reading that back at once takes 36 us.
 #include <type_traits>
 
 #include "q4_cache.hpp"
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(Cache c, Batch b, 
 
 // Kv heads that a workgroup takes in turn, so that the search for its place is made once:
 // up to eight, of sixteen workgroups a compute unit or more.  (One, two, four, eight:
-// reading 400 MB of cache to fp16 565, 502, 437, 426 us; 37 MB of it to bf16 46, 39, 36
+// reading 401 MB of cache to fp16 565, 502, 437, 426 us; 44 MB of it to bf16 46, 39, 36
 // and 41 us, as so few workgroups do not come out even; writing those 68, 55, 53, 53.)
 int heads_in_turn(const Cache& c, int64_t places) {
   const int64_t plenty = places * c.kv_heads / (16 * static_cast<int64_t>(device_cu_count()));
