@@ -212,8 +212,8 @@ __global__ __launch_bounds__(kWaves* kWave) void attention_row_kernel(Attention 
     }
     const int token = r / a.group;
     const int64_t out = static_cast<int64_t>(q.row + token) * a.heads + h * a.group + r - token * a.group;
-    store_as(a.y, a.y_dt, out * D + e, sum > 0.f ? v / sum : 0.f);
-    if (a.lse != nullptr && e == 0) a.lse[out] = sum > 0.f ? top + logf(sum) : -INFINITY;
+    store_as(a.y, a.y_dt, out * D + e, sum != 0.f ? v / sum : 0.f);
+    if (a.lse != nullptr && e == 0) a.lse[out] = sum != 0.f ? top + logf(sum) : -INFINITY;
   }
 }
 
@@ -242,8 +242,8 @@ __global__ __launch_bounds__(kWaves* kWave) void attention_row_join_kernel(Atten
     }
     const int token = r / a.group;
     const int64_t out = static_cast<int64_t>(q.row + token) * a.heads + h * a.group + r - token * a.group;
-    store_as(a.y, a.y_dt, out * dim + e, sum > 0.f ? v / sum : 0.f);
-    if (a.lse != nullptr && e == 0) a.lse[out] = sum > 0.f ? top + logf(sum) : -INFINITY;
+    store_as(a.y, a.y_dt, out * dim + e, sum != 0.f ? v / sum : 0.f);
+    if (a.lse != nullptr && e == 0) a.lse[out] = sum != 0.f ? top + logf(sum) : -INFINITY;
   }
 }
 

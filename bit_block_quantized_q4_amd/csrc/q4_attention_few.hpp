@@ -500,14 +500,14 @@ __device__ __forceinline__ void attention_few(const Attention& a, const Few& f, 
         const int r = r0 + nt * 16 + m16;
         const int i = r / a.group;
         const int64_t at = static_cast<int64_t>(q.row + i) * a.heads + h * a.group + (r - i * a.group);
-        const float inverse = sum > 0.f ? 1.f / sum : 0.f;
+        const float inverse = sum != 0.f ? 1.f / sum : 0.f;
         if (wave == 0 && g == 0) {
           if (!done) {
             float* st = f.parts.stats + (slot * R + nt * 16 + m16) * 2;
             st[0] = top;
             st[1] = sum;
           } else if (r < rows && a.lse != nullptr) {
-            a.lse[at] = sum > 0.f ? (top - kLift + log2f(sum)) * kLn2 : -INFINITY;
+            a.lse[at] = sum != 0.f ? (top - kLift + log2f(sum)) * kLn2 : -INFINITY;
           }
         }
 #pragma unroll
@@ -591,11 +591,11 @@ __device__ __forceinline__ void store_joined(const Attention& a, const int4& not
   if (r >= q.rows * a.group) return;
   const int token = r / a.group, h = static_cast<int>(static_cast<uint32_t>(note.w) >> 16);
   const int64_t at = static_cast<int64_t>(q.row + token) * a.heads + h * a.group + (r - token * a.group);
-  const float inverse = o.sum > 0.f ? 1.f / o.sum : 0.f;
+  const float inverse = o.sum != 0.f ? 1.f / o.sum : 0.f;
   const float out[4] = {o.v[0] * inverse, o.v[1] * inverse, o.v[2] * inverse, o.v[3] * inverse};
   store4(a.y, a.y_dt, at * (NB * kQK) + blk * kQK + e * 16 + 4 * g, out);
   if (a.lse != nullptr && g == 0 && e == 0 && blk == 0)
-    a.lse[at] = o.sum > 0.f ? (o.top - kLift + log2f(o.sum)) * kLn2 : -INFINITY;
+    a.lse[at] = o.sum != 0.f ? (o.top - kLift + log2f(o.sum)) * kLn2 : -INFINITY;
 }
 
 // Many notes, few parts each: a workgroup takes 16 rows of half the columns (e) of a note,

@@ -475,7 +475,7 @@ __device__ __forceinline__ void attention_many(const Attention& a, const Many& y
   }
   if (w0 + n >= end_row) return;
   const int64_t at = static_cast<int64_t>(q.row + token) * a.heads + hq;
-  const float inverse = l > 0.f ? 1.f / l : 0.f;
+  const float inverse = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -484,7 +484,7 @@ __device__ __forceinline__ void attention_many(const Attention& a, const Many& y
                             o[b][4 * i + 3] * inverse};
       store4(a.y, a.y_dt, at * (NB * kQK) + b * kQK + 8 * i + 4 * half, out);
     }
-  if (a.lse != nullptr && half == 0) a.lse[at] = l > 0.f ? (m - kLift2 + log2f(l)) * kLn2 : -INFINITY;
+  if (a.lse != nullptr && half == 0) a.lse[at] = l != 0.f ? (m - kLift2 + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // The splits' parts of a row tile, in their order; a wavefront takes 32 rows (of
@@ -518,13 +518,13 @@ __device__ __forceinline__ void attention_splits(const Attention& a, const Many&
     if (row >= rows) continue;
     const int token = row / a.group;
     const int64_t at = static_cast<int64_t>(q.row + token) * a.heads + h * a.group + row - token * a.group;
-    const float inverse = l > 0.f ? 1.f / l : 0.f;
+    const float inverse = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float out[4] = {v[j][0] * inverse, v[j][1] * inverse, v[j][2] * inverse, v[j][3] * inverse};
       store4(a.y, a.y_dt, at * (NB * kQK) + b * kQK + 8 * j + 4 * half, out);
     }
-    if (a.lse != nullptr && half == 0 && b == 0) a.lse[at] = l > 0.f ? (m - kLift2 + log2f(l)) * kLn2 : -INFINITY;
+    if (a.lse != nullptr && half == 0 && b == 0) a.lse[at] = l != 0.f ? (m - kLift2 + log2f(l)) * kLn2 : -INFINITY;
   }
 }
 

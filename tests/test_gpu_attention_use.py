@@ -2,6 +2,8 @@
 attention from its products on, captured and replayed decode steps, two streams, caches
 of more than 4 GiB, prefixes that sequences share, thousands of sequences."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -292,3 +294,24 @@ def test_batches_that_make_no_sense(q4lib, gpu, dtype):
                 want, bound, _, _ = attention64(q[lo:hi], cache, b)
                 check(y[lo:hi], want, bound, str((lengths, offsets, s)))
         assert (y.cpu()[free] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("name", BATCHES)
+def test_rows_that_are_no_numbers(q4lib, gpu, dtype, name):
+    """NaN or an infinity in a row and head of q: that one has no number in y and lse, every other one
+    the same bits."""
+    b, cache, q, args = example(name, gpu, dtype)
+    want = q4lib.q4_attention(*args)
+    row, head = b.places[len(b.places) // 2][0], q.shape[1] // 2
+    for bad in (math.nan, math.inf, -math.inf):
+        x = args[0].clone()
+        x[row, head, 3] = bad
+        y, lse = q4lib.q4_attention(x, *args[1:], return_lse=True)
+        others = torch.zeros(b.tokens, q.shape[1], dtype=torch.bool, device=gpu)
+        for r, *_ in b.places:
+            others[r] = True
+        others[row, head] = False
+        assert torch.equal(y[others], want[others]), bad
+        if math.isnan(bad) and b.lengths[b.places[len(b.places) // 2][1]] > 0:
+            assert y[row, head].isnan().all() and lse[row, head].isnan()
