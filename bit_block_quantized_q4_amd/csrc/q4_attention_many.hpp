@@ -537,9 +537,27 @@ inline int64_t many_places(const Attention& a) {
 // Workgroups that a compute unit holds, by their registers.
 inline int many_per_unit(int dim) { return dim > 128 ? 1 : dim > 64 ? 2 : 3; }
 
+// Parts of the positions where there are fewer row tiles than workgroups at once: the
+// number that lets the fewest turns of all workgroups do, the smallest such.  Places of
+// sequences without a tile start workgroups too, of which a quarter more than at once is
+// enough.  (256 rows of each of two sequences behind 16128 positions, heads of 256: whole
+// 955 us, in two parts 509; heads of 128 215 and 174.)
 inline int many_splits(const Attention& a) {
-  const int64_t n = many_places(a) * a.cache.kv_heads, room = device_cu_count() * many_per_unit(a.cache.dim);
-  return n >= room ? 1 : static_cast<int>(room / n < 32 ? room / n : 32);
+  const int64_t room = device_cu_count() * static_cast<int64_t>(many_per_unit(a.cache.dim));
+  const int64_t rows = static_cast<int64_t>(a.batch.tokens) * a.group;
+  const int64_t n = (rows + kManyRows - 1) / kManyRows * a.cache.kv_heads;
+  if (n >= room) return 1;
+  const int64_t most = 5 * room / (4 * many_places(a) * a.cache.kv_heads);
+  int best = 1;
+  int64_t turns = 1;  // of best, each the best-th part of the positions
+  for (int s = 2; s <= most && s <= 32; ++s) {
+    const int64_t mine = (n * s + room - 1) / room;
+    if (mine * best < turns * s) {
+      best = s;
+      turns = mine;
+    }
+  }
+  return best;
 }
 
 inline size_t many_stats_bytes(const Attention& a, int splits) {
