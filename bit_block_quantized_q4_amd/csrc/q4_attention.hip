@@ -73,6 +73,7 @@ __global__ __launch_bounds__(kWaves* kWave) void attention_row_kernel(Attention 
   }
   __syncthreads();
   const int64_t to_values = static_cast<int64_t>(a.cache.per_page) * (9 * D);
+  const Cap<false> cap(a.softcap);
 
   float m[R], l[R], acc[R][C][2];  // l: this lane's positions; acc: columns i and i + 16 of byte column lane + 64 c
 #pragma unroll
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(kWaves* kWave) void attention_row_kernel(Attention 
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       x[j] *= a.scale;
-      if (a.softcap > 0.f) x[j] = capped(x[j], a.softcap);
+      if (a.softcap > 0.f) x[j] = cap.of(x[j]);
       if (g == nullptr || t < lo[j] || t >= hi[j]) x[j] = -INFINITY;
       float top = max_over_groups(x[j]);
 #pragma unroll

@@ -16,19 +16,38 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLift = 12.f;
 
-// c tanh(s / c) as c - 2 c / (exp(2 s / c) + 1): +-c where exp leaves fp32.
-__device__ __forceinline__ float capped(float s, float c) {
-  return c - 2.f * c / (exp2f(2.f * kLog2e * s / c) + 1.f);
-}
-
-// The same from s and back in units of log2, for many scores: as c - 2 c / (e + 1) with
-// the reciprocal of the hardware (1 ulp).
+// c tanh(z), z = s / c, from s: in units of log2 (LOG2) or natural, with an error of some
+// 5 2^-24 of the result whatever c is.
+//   |z| <= kNear: s times an even polynomial, tanh(z) / z = 1 + z^2 (..), fitted to 2^-27.
+//   above: t = exp(-2 |z|), 1 - 2 t / (1 + t), exp and reciprocal of the hardware (1 ulp).
+// (The second form alone leaves an error of 2^-24 c, which for a c of 10^6 is 0.1.)  Scores
+// of a tile that are all near, as they mostly are, take the polynomial alone: two
+// transcendental instructions less each.
+template <bool LOG2>
 struct Cap {
-  float c, in, out;
-  __device__ __forceinline__ explicit Cap(float cap) : c(cap * kLog2e), in(2.f * kLog2e / cap), out(-2.f * cap * kLog2e) {}
+  static constexpr float kNear = 0.625f, kUnit = LOG2 ? kLog2e : 1.f;
+  float top, in;
+  // (both the same on all lanes, kept in scalar registers; a c below 2^-128 has no
+  // reciprocal in fp32)
+  __device__ __forceinline__ explicit Cap(float c)
+      : top(uniform(c * kUnit)), in(uniform(fminf(1.f / c, 3.4028234e38f))) {}
+  static __device__ __forceinline__ float uniform(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+  }
+  // Whether scores of up to this magnitude are near.
+  __device__ __forceinline__ bool near(float most) const { return most * in <= kNear; }
+  __device__ __forceinline__ float of_near(float s) const {
+    const float z = s * in, u = z * z;
+    float p = fmaf(u, -0.00570498f * kUnit, 0.02063908f * kUnit);
+    p = fmaf(u, p, -0.05373971f * kUnit);
+    p = fmaf(u, p, 0.13331442f * kUnit);
+    p = fmaf(u, p, -0.33333282f * kUnit);
+    return s * fmaf(u, p, kUnit);
+  }
   __device__ __forceinline__ float of(float s) const {
-    const float e = __builtin_amdgcn_exp2f(s * in);
-    return fmaf(out, __builtin_amdgcn_rcpf(e + 1.f), c);
+    const float z = fabsf(s * in), t = __builtin_amdgcn_exp2f(-2.f * kLog2e * z);
+    const float far = __builtin_copysignf(fmaf(-2.f * t, __builtin_amdgcn_rcpf(1.f + t), 1.f), s) * top;
+    return z <= kNear ? of_near(s) : far;
   }
 };
 

@@ -195,7 +195,7 @@ __device__ __forceinline__ void attention_few(const Attention& a, const Few& f, 
     int64_t job = f.whole ? unit - base : (unit - base) / w.tiles;
     int t0 = f.whole ? 0 : static_cast<int>(unit - base - job * w.tiles);
     const UnpackConsts uc = make_unpack_consts();
-    const Cap cap(a.softcap);
+    const Cap<true> cap(a.softcap);
 
     while (unit < end) {
       while (job >= static_cast<int64_t>(w.row_tiles) * c.kv_heads) {
@@ -382,8 +382,16 @@ __device__ __forceinline__ void attention_few(const Attention& a, const Few& f, 
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[nt][e] *= mul[nt];
           if (a.softcap > 0.f) {
+            float most = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[nt][e] = cap.of(x[nt][e]);
+            for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(x[nt][e]));
+            if (__all(cap.near(most))) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[nt][e] = cap.of_near(x[nt][e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[nt][e] = cap.of(x[nt][e]);
+            }
           }
           if (!whole) {
             const int from = lo[nt] - first - 16 * g, to = named_v ? hi[nt] - first - 16 * g : 0;

@@ -146,7 +146,7 @@ __device__ __forceinline__ void attention_many(const Attention& a, const Many& y
   if (!job_of<R>(a, y, block, &s, &h, &r0, &rows, &split, &q)) return;
   const Cache& c = a.cache;
   const UnpackConsts uc = make_unpack_consts();
-  const Cap cap(a.softcap);
+  const Cap<true> cap(a.softcap);
 
   // The tiles of all the workgroup's rows, and of this part of them.
   const int end_row = r0 + R < rows ? r0 + R : rows;
@@ -369,9 +369,21 @@ __device__ __forceinline__ void attention_many(const Attention& a, const Many& y
     if (a.softcap > 0.f) {
       by = 1.f;
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < 2; ++mt) {
+        float most = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[mt][i] = cap.of(x[mt][i] * mul);
+        for (int i = 0; i < 16; ++i) {
+          x[mt][i] *= mul;
+          most = fmaxf(most, fabsf(x[mt][i]));
+        }
+        if (__all(cap.near(most))) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[mt][i] = cap.of_near(x[mt][i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[mt][i] = cap.of(x[mt][i]);
+        }
+      }
     }
     if (!(t >= whole0 && t < whole1 && all)) {
       const int first = t * kTile;

@@ -1,0 +1,49 @@
+"""Attention over the paged Q4_0 cache at calls that once went wrong."""
+
+import pytest
+import torch
+
+from _attention_bounds import attention_bounds
+from _cache import TYPES, Batch, check, random_cache, rows
+
+pytestmark = pytest.mark.gpu
+
+# (batch, heads, kv heads, d): one position; one row each, cut and not; drafts in products of 16 and of 32
+# rows; prompts; both in one batch
+WAYS = {
+    "single": (Batch([1] * 60, [1] * 60, 16, seed=1, single=True), 4, 2, 32),
+    "tokens": (Batch([5000, 700, 1], [1] * 3, 16, single=True), 8, 2, 128),
+    "whole": (Batch([100, 400, 7], [1] * 3, 16, seed=3, single=True), 40, 2, 64),
+    "drafts": (Batch([900, 1300, 40], [5, 2, 3], 16, seed=4), 10, 2, 128),
+    "prompts": (Batch([150, 400], [150, 90], 128, seed=6), 4, 4, 64),
+    "mixed": (Batch([900, 700, 300], [1, 50, 120], 16, seed=5, before=1, behind=3), 4, 1, 96),
+    "wide": (Batch([330, 90], [100, 1], 32, seed=7), 4, 2, 256),
+}
+
+
+def example(name, dtype, seed=1):
+    b, heads, kv, d = WAYS[name]
+    return b, random_cache(seed, b.pages, kv, b.page, d), rows(seed + 1, dtype, b.tokens, heads, d)
+
+
+def same(q4lib, gpu, b, cache, q, what, y_dtype=None, **kw):
+    y = torch.full(q.shape, 7.0, dtype=y_dtype or q.dtype, device=gpu)
+    lse = torch.full(q.shape[:2], 7.0, device=gpu)
+    q4lib.q4_attention(q.to(gpu), torch.from_numpy(cache).to(gpu), *b.device(gpu), return_lse=True, y=y, lse=lse, **kw)
+    want, bound, big, lbound = attention_bounds(q, cache, b, dtype=y.dtype, **kw)
+    check(y, want, bound, what)
+    check(lse, big, lbound, "lse " + what)
+
+
+# ------------------------------------------------------------------ caps
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("name", WAYS)
+@pytest.mark.parametrize("softcap", [1e-40, 1e-3, 0.7, 30.0, 1e3, 1e6, 1e30, 3e38])
+def test_caps_of_every_size(q4lib, gpu, dtype, name, softcap):
+    """A cap far above the scores leaves them as they are, one far below makes them all alike;
+    rows whose scores reach a cap of 1000 beside rows whose scores are some few."""
+    b, cache, q = example(name, dtype)
+    for row, _, _ in b.places[::3]:
+        q[row, 1] *= 1000
+    same(q4lib, gpu, b, cache, q, f"{dtype} {name} cap {softcap}", softcap=softcap)
