@@ -58,8 +58,9 @@ __global__ __launch_bounds__(kWaves* kWave) void attention_row_kernel(Attention 
   if (!job_of<R>(a, y, blockIdx.x, &s, &h, &r0, &rows, &split, &q)) return;
   for (int i = threadIdx.x; i < R * D; i += kWaves * kWave) {
     const int j = i / D, e = i - j * D, r = r0 + j < rows ? r0 + j : rows - 1, token = r / a.group;
-    lds.q[e][j] = static_cast<const float*>(a.q)[(q.row + token) * a.q_stride +
-                                                 static_cast<int64_t>(h * a.group + r - token * a.group) * D + e];
+    const float v = static_cast<const float*>(a.q)[(q.row + token) * a.q_stride +
+                                                   static_cast<int64_t>(h * a.group + r - token * a.group) * D + e];
+    lds.q[e][j] = fmaf(v, 0.f, v);  // (NaN of an infinity: see query_pair)
   }
   int lo[R], hi[R], first = 0x7FFFFFFF, end = 0;  // what each row sees, and all together
 #pragma unroll

@@ -51,6 +51,14 @@ struct Cap {
   }
 };
 
+// f q (f 0 or +-1) of two values of q; NaN of an infinite one, so that every product with it
+// is NaN, also with a code or a scale of 0.
+__device__ __forceinline__ uint32_t query_pair(uint32_t q, float f) {
+  const half2_t v = __builtin_bit_cast(half2_t, q);
+  const half_t h = static_cast<half_t>(f), z = static_cast<half_t>(0.f);
+  return __builtin_bit_cast(uint32_t, v * half2_t{h, h} + v * half2_t{z, z});
+}
+
 // The larger / the sum of the values that the lanes of the same l % 16 hold.
 __device__ __forceinline__ float max_over_groups(float v) {
   const uint32_t b = __builtin_bit_cast(uint32_t, v);

@@ -257,8 +257,8 @@ __device__ __forceinline__ void attention_few(const Attention& a, const Few& f, 
           u32x4 v;  // elements (0, 2), (1, 3), (16, 18), (17, 19) from 4 g on
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            v[2 * e] = __builtin_amdgcn_perm(part[blk][e].y, part[blk][e].x, 0x05040100);
-            v[2 * e + 1] = __builtin_amdgcn_perm(part[blk][e].y, part[blk][e].x, 0x07060302);
+            v[2 * e] = query_pair(__builtin_amdgcn_perm(part[blk][e].y, part[blk][e].x, 0x05040100), 1.f);
+            v[2 * e + 1] = query_pair(__builtin_amdgcn_perm(part[blk][e].y, part[blk][e].x, 0x07060302), 1.f);
           }
           qf[nt][blk] = __builtin_bit_cast(half8_t, v);
         }

@@ -204,16 +204,16 @@ __device__ __forceinline__ void attention_many(const Attention& a, const Many& y
         }
     }
     // The factor is positive, so that the largest score is the largest product's: a
-    // negative scale turns q, one of 0 clears it.
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u, keep = a.scale == 0.f ? 0u : ~0u;
+    // negative scale turns q, one of 0 clears it (but what is no number).
+    const float sign = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
     mul = fmaxf(mul, 1.17549435e-38f);
 #pragma unroll
     for (int i = 0; i < 2 * NB; ++i) {
       u32x4 v;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        v[2 * e] = __builtin_amdgcn_perm(part[i][e].y, part[i][e].x, 0x05040100) & keep ^ flip;
-        v[2 * e + 1] = __builtin_amdgcn_perm(part[i][e].y, part[i][e].x, 0x07060302) & keep ^ flip;
+        v[2 * e] = query_pair(__builtin_amdgcn_perm(part[i][e].y, part[i][e].x, 0x05040100), sign);
+        v[2 * e + 1] = query_pair(__builtin_amdgcn_perm(part[i][e].y, part[i][e].x, 0x07060302), sign);
       }
       qf[i] = __builtin_bit_cast(half8_t, v);
     }

@@ -417,8 +417,9 @@ q4_status q4_cache_read(const q4_cache *cache, const q4_batch *batch, void *k, v
  *   s_t = scale q . k_t;  softcap > 0: s_t = softcap tanh(s_t / softcap)
  *   y   = sum_t exp(s_t) v_t / sum_t exp(s_t),  lse = ln sum_t exp(s_t)
  * It sees t < lengths[s], with `causal` t <= p, with window > 0 t > p - window.
- * A row that sees nothing has y = 0, lse = -infinity; one whose q holds a NaN, or
- * whose scores do not all compare (an infinite q), has NaN in both. */
+ * A row that sees nothing has y = 0, lse = -infinity; any other whose q holds a NaN
+ * or an infinity has NaN in both.  q . k and s_t are below 2^126 in magnitude: a
+ * larger one may count as an infinity. */
 typedef struct q4_attention_options {
   float scale;    /* finite */
   int causal;     /* 0 or 1 */

@@ -1,5 +1,7 @@
 """Attention over the paged Q4_0 cache at calls that once went wrong."""
 
+import math
+
 import pytest
 import torch
 
@@ -47,3 +49,45 @@ def test_caps_of_every_size(q4lib, gpu, dtype, name, softcap):
     for row, _, _ in b.places[::3]:
         q[row, 1] *= 1000
     same(q4lib, gpu, b, cache, q, f"{dtype} {name} cap {softcap}", softcap=softcap)
+
+
+# ------------------------------------------------------------------ rows that are no numbers
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("name", WAYS)
+@pytest.mark.parametrize("kw", [dict(), dict(scale=0.0), dict(scale=-0.3, window=40), dict(softcap=20.0),
+                                dict(scale=0.0, softcap=1e6)])
+def test_nan_and_infinities_in_q(q4lib, gpu, dtype, name, kw):
+    """One of them anywhere in a row and head of q is NaN in its y and lse, whatever the scale and
+    the cap, also where the row sees a single position; other rows and heads have the same bits."""
+    b, cache, q = example(name, dtype)
+    args = [torch.from_numpy(cache).to(gpu)] + b.device(gpu)
+    mine = torch.zeros(q.shape[:2], dtype=torch.bool, device=gpu)
+    for row, _, _ in b.places:
+        mine[row] = True
+    want = q4lib.q4_attention(q.to(gpu), *args, return_lse=True, **kw)
+    for i, bad in enumerate((math.nan, math.inf, -math.inf)):
+        x, others = q.clone(), mine.clone()
+        hit = [(b.places[j][0], (j + i) % q.shape[1]) for j in {0, len(b.places) // 2, len(b.places) - 1}]
+        for row, head in hit:
+            x[row, head, (row + 5 * i) % q.shape[2]] = bad
+            others[row, head] = False
+        y, lse = q4lib.q4_attention(x.to(gpu), *args, return_lse=True, **kw)
+        assert torch.equal(y[others], want[0][others]) and torch.equal(lse[others], want[1][others]), bad
+        for row, head in hit:
+            assert y[row, head].isnan().all() and lse[row, head].isnan(), (bad, row, head)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("counts", [[1, 1, 1], [3, 4, 2], [50, 60, 40]])
+def test_nan_in_rows_that_see_nothing(q4lib, gpu, dtype, counts):
+    """They have y 0 and lse -infinity as any such row: no positions, or no page for any."""
+    b = Batch([0, 70, 90], counts, 16, single=counts[0] == 1)
+    b.tables[1] = -1
+    cache, q = random_cache(1, b.pages, 2, 16, 64), rows(2, dtype, b.tokens, 4, 64)
+    q[::2, :, 7], q[1::2, :, 9] = math.nan, math.inf
+    for kw in (dict(), dict(scale=0.0), dict(softcap=5.0)):
+        y, lse = q4lib.q4_attention(q.to(gpu), torch.from_numpy(cache).to(gpu), *b.device(gpu), return_lse=True, **kw)
+        n = counts[0] + counts[1]
+        assert (y[:n] == 0).all() and (lse[:n] == -math.inf).all()
+        assert y[n:].isnan().all() and lse[n:].isnan().all()
