@@ -804,10 +804,7 @@ def _row_stride(t, name, heads, head_dim):
     """Elements between the rows of t [tokens, heads, head_dim], whose heads lie together."""
     if t.dim() != 3 or (heads and t.shape[1] != heads) or t.shape[2] != head_dim:
         raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {head_dim}]; got {tuple(t.shape)}")
-    if t.shape[0] > 1 or t.stride(0) >= t.shape[1] * head_dim:
-        stride = t.stride(0)
-    else:  # one row: its stride says nothing
-        stride = t.shape[1] * head_dim
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * head_dim  # (of one row it says nothing)
     if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim):
         raise ValueError(f"{name}'s heads must lie together (only rows may have a stride)")
     return stride

@@ -324,7 +324,7 @@ struct CacheCall {
   int64_t stride(Call& c, const at::Tensor& t) {
     const int64_t width = t.size(1) * cache.head_dim;
     c.want(t.size(2) == cache.head_dim && t.stride(2) == 1 && (t.size(1) == 1 || t.stride(1) == cache.head_dim));
-    return t.size(0) > 1 || t.stride(0) >= width ? t.stride(0) : width;
+    return t.size(0) > 1 ? t.stride(0) : width;  // (of one row it says nothing)
   }
 };
 

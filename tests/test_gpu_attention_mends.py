@@ -91,3 +91,28 @@ def test_nan_in_rows_that_see_nothing(q4lib, gpu, dtype, counts):
         n = counts[0] + counts[1]
         assert (y[:n] == 0).all() and (lse[:n] == -math.inf).all()
         assert y[n:].isnan().all() and lse[n:].isnan().all()
+
+
+# ------------------------------------------------------------------ strides
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_one_row_of_rows_that_are_no_whole_pieces_apart(q4lib, gpu, dtype):
+    """The first of rows that lie an odd number of elements apart: a row alone has no stride."""
+    b = Batch([37], [1], 16, single=True)
+    cache = torch.from_numpy(random_cache(1, b.pages, 2, 16, 64)).to(gpu)
+    tables, lengths, _ = b.device(gpu)
+    wide = rows(2, dtype, 3, 8 * 64 + 1).to(gpu)
+    qkv = wide.as_strided((1, 8, 64), (8 * 64 + 1, 64, 1))
+    q, k, v = qkv[:, :4], qkv[:, 4:6], qkv[:, 6:]
+    assert q.stride(0) == 8 * 64 + 1
+    one, two = cache.clone(), cache.clone()
+    q4lib.q4_cache_write(k.contiguous(), v.contiguous(), one, tables, lengths)
+    want = q4lib.q4_attention(q.contiguous(), one, tables, lengths)
+    q4lib.q4_cache_write(k, v, two, tables, lengths)
+    assert torch.equal(one, two)
+    assert torch.equal(q4lib.q4_attention(q, two, tables, lengths), want)
+    y = torch.empty_like(want)
+    assert torch.equal(q4lib.q4_attention(q, two, tables, lengths, y=y), want)
+    fast = q4lib._fast()
+    assert fast.cache_write(k, v, two, tables, lengths, None) is True
+    assert torch.equal(fast.attention(q, two, tables, lengths, None, None, True, 0, 0.0, False), want)
