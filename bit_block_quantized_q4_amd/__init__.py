@@ -869,7 +869,7 @@ def q4_cache_read(cache, tables, lengths, offsets=None, tokens=None, dtype=None,
         if fast is not None:
             code = 1 if dtype is None or dtype is torch.float16 else 2 if dtype is torch.bfloat16 else (
                 0 if dtype is torch.float32 else -1)
-            out = fast.cache_read(cache, tables, lengths, offsets, -1 if tokens is None else tokens, code)
+            out = fast.cache_read(cache, tables, lengths, offsets, tokens, code)
             if out is not None:
                 return out
     index = _same_device_rows(cache, {}, cache=cache, tables=tables, lengths=lengths, offsets=offsets, k=k, v=v)

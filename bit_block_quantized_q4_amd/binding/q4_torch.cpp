@@ -348,13 +348,14 @@ PyObject* cache_write(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// A cache call, tokens (-1: one a sequence), dtype (0, 1, 2 as in q4_dtype) -> (k, v)
+// A cache call, tokens (None: one a sequence), dtype (0, 1, 2 as in q4_dtype) -> (k, v)
 PyObject* cache_read(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (n != 6) return nullptr;
     Call c{args};
-    const int64_t tokens = PyLong_Check(args[4]) ? PyLong_AsLongLong(args[4]) : 0, dt = c.integer(5);
-    c.want(tokens >= 1 || (tokens == -1 && args[3] == Py_None));
+    const bool each = args[4] == Py_None;
+    const int64_t tokens = each ? -1 : c.integer(4), dt = c.integer(5);
+    c.want(each ? args[3] == Py_None : tokens >= 1);
     CacheCall cc;
     if (!c.ok || dt < 0 || dt > 2 || !cc.take(c, 0, tokens) || !c.ready()) return nullptr;
     const auto options =

@@ -116,3 +116,18 @@ def test_one_row_of_rows_that_are_no_whole_pieces_apart(q4lib, gpu, dtype):
     fast = q4lib._fast()
     assert fast.cache_write(k, v, two, tables, lengths, None) is True
     assert torch.equal(fast.attention(q, two, tables, lengths, None, None, True, 0, 0.0, False), want)
+
+
+# ------------------------------------------------------------------ numbers of rows
+
+@pytest.mark.parametrize("with_offsets", [False, True])
+@pytest.mark.parametrize("tokens", [-1, 0, 1 << 63, 1 << 70])
+def test_numbers_of_rows_that_are_none(q4lib, gpu, tokens, with_offsets):
+    """Reading back refuses them (-1 was taken for one row a sequence)."""
+    b = Batch([37, 5], [1, 1], 16)
+    cache = q4lib.q4_cache(b.pages, 16, 2, 64, device=gpu)
+    tables, lengths, offsets = b.device(gpu)
+    with pytest.raises((ValueError, RuntimeError, TypeError)):
+        q4lib.q4_cache_read(cache, tables, lengths, offsets if with_offsets else None, tokens=tokens)
+    k, _ = q4lib.q4_cache_read(cache, tables, lengths)
+    assert k.shape == (2, 2, 64)
