@@ -34,7 +34,7 @@ import math
 import numpy as np
 import torch
 
-from _cache import HALF, TINY, U, sequence
+from _cache import HALF, TINY, U, Batch, random_cache, rows, sequence
 
 FEW_ROWS = 32
 
@@ -48,6 +48,24 @@ def way_of(batch, s, group, dtype):
 def two_parts(batch, way, group, d, dtype):
     wide = d <= 192 and (batch.offsets is None or d > 64) and batch.tokens * group > 16 * batch.seqs
     return way == "few" and dtype == torch.float16 and not wide
+
+
+# Batches of few rows over few positions, where what a score or a weight is rounded to shows:
+# lse of one position is its score, and a weight is a good part of all.
+FEW = {
+    "single": (Batch([1] * 60, [1] * 60, 16, single=True), 4, 2, 64),
+    "tokens": (Batch([2, 3, 5, 9, 17, 40], [1] * 6, 16, seed=1, single=True), 4, 2, 64),
+    "drafts": (Batch([2, 9, 17, 40], [2, 3, 1, 4], 16, seed=2), 4, 2, 128),
+}
+
+
+def few_example(name, dtype, seed=1):
+    """A batch, its cache, whose values fp16 holds exactly, and q."""
+    b, heads, kv, d = FEW[name]
+    cache = random_cache(seed, b.pages, kv, b.page, d)
+    scales = np.ascontiguousarray(cache[:, :, 1, :, 8 * d:]).view(np.uint16)
+    cache[:, :, 1, :, 8 * d:] = (scales & 0xFC00).view(np.uint8)  # powers of two
+    return b, cache, rows(seed + 1, dtype, b.tokens, heads, d, scale=0.5)
 
 
 def to_half(x):

@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from _attention_bounds import attention_bounds
+from _attention_bounds import FEW, attention_bounds, few_example
 from _cache import TYPES, Batch, check, random_cache, rows
 
 pytestmark = pytest.mark.gpu
@@ -131,3 +131,23 @@ def test_numbers_of_rows_that_are_none(q4lib, gpu, tokens, with_offsets):
         q4lib.q4_cache_read(cache, tables, lengths, offsets if with_offsets else None, tokens=tokens)
     k, _ = q4lib.q4_cache_read(cache, tables, lengths)
     assert k.shape == (2, 2, 64)
+
+
+# ------------------------------------------------------------------ what is rounded
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("name", FEW)
+@pytest.mark.parametrize("kw", [dict(), dict(window=3), dict(softcap=2.0), dict(scale=-0.5)])
+def test_few_rows_round_neither_keys_nor_weights_of_fp16_q(q4lib, gpu, dtype, name, kw):
+    """Keys' codes and scales as they are, weights of fp16 q in two parts: held to bounds that
+    a key rounded to fp16, or a weight in one part, leaves."""
+    b, cache, q = few_example(name, dtype)
+    same(q4lib, gpu, b, cache, q, f"{dtype} {name} {kw}", y_dtype=torch.float32, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("name", WAYS)
+@pytest.mark.parametrize("kw", [dict(), dict(window=70), dict(causal=False), dict(scale=-0.3)])
+def test_every_way_within_what_it_rounds(q4lib, gpu, dtype, name, kw):
+    b, cache, q = example(name, dtype)
+    same(q4lib, gpu, b, cache, q, f"{dtype} {name} {kw}", y_dtype=torch.float32, **kw)
