@@ -261,12 +261,13 @@ __device__ __forceinline__ void attention_many(const Attention& a, const Many& y
       p += to_values;
 #pragma unroll
       for (int i = 0; i < (NB + 3) / 4; ++i) {
-        const int at = 64 * i + lane;  // block at / 16, byte at % 16
-        if (64 * i + 64 <= 16 * NB || at < 16 * NB) {
-          bytes.v[i] = *reinterpret_cast<const u32x4*>(p + at * 16);
-          bytes.vs[i][0] = *reinterpret_cast<const u32x4*>(p + 256 * NB + at / 16 * 32);
-          bytes.vs[i][1] = *reinterpret_cast<const u32x4*>(p + 256 * NB + at / 16 * 32 + 16);
-        }
+        // Block at / 16, byte at % 16.  Lanes beyond the last one load it again: without a
+        // branch here.  (At one in the kernel of 192 columns, which is short of registers,
+        // the compiler moved values that all lanes need while some did not take part.)
+        const int at = 64 * i + lane < 16 * NB ? 64 * i + lane : 16 * NB - 1;
+        bytes.v[i] = *reinterpret_cast<const u32x4*>(p + at * 16);
+        bytes.vs[i][0] = *reinterpret_cast<const u32x4*>(p + 256 * NB + at / 16 * 32);
+        bytes.vs[i][1] = *reinterpret_cast<const u32x4*>(p + 256 * NB + at / 16 * 32 + 16);
       }
     }
   };

@@ -151,3 +151,20 @@ def test_few_rows_round_neither_keys_nor_weights_of_fp16_q(q4lib, gpu, dtype, na
 def test_every_way_within_what_it_rounds(q4lib, gpu, dtype, name, kw):
     b, cache, q = example(name, dtype)
     same(q4lib, gpu, b, cache, q, f"{dtype} {name} {kw}", y_dtype=torch.float32, **kw)
+
+
+# ------------------------------------------------------------------ positions that are not split
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d,heads", [(32, 400), (64, 400), (96, 160), (128, 160), (160, 80), (192, 80), (224, 80),
+                                     (256, 80)])
+@pytest.mark.parametrize("empty", [0, 40])
+def test_prompts_of_as_many_workgroups_as_there_is_room_for(q4lib, gpu, dtype, d, heads, empty):
+    """Rows leave the workgroup that has all their positions (with fewer workgroups the positions are
+    split and the rows joined by another launch); alone, and where the batch's rows are few on
+    average."""
+    n = 500
+    b = Batch([n + 30] + [3] * empty, [n] + [0] * empty, 64, seed=d)
+    assert (n + 127) // 128 * heads >= 256 * (1 if d > 128 else 2 if d > 64 else 3)
+    cache, q = random_cache(1, b.pages, heads, 64, d), rows(2, dtype, b.tokens, heads, d)
+    same(q4lib, gpu, b, cache, q, f"{dtype} {heads} x {d}")
