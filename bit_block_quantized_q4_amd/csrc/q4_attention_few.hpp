@@ -381,7 +381,7 @@ __device__ __forceinline__ void attention_few(const Attention& a, const Few& f, 
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[nt][e] *= mul[nt];
-          if (a.softcap > 0.f) {
+          if (__builtin_expect(a.softcap > 0.f, 0)) {
             float most = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(x[nt][e]));

@@ -367,7 +367,9 @@ __device__ __forceinline__ void attention_many(const Attention& a, const Many& y
   auto weights = [&](int t) __attribute__((always_inline)) {
     const bool all = __builtin_amdgcn_readfirstlane(there.x & there.y & there.z & there.w) != 0;
     float by = mul;
-    if (a.softcap > 0.f) {
+    // (As an unlikely way: with its code in line a prompt of 4000, 32 heads of 256 on 8, takes
+    // 493 us, so 478; of 192 407 and 401.)
+    if (__builtin_expect(a.softcap > 0.f, 0)) {
       by = 1.f;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
