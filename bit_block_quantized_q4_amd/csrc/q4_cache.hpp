@@ -126,7 +126,7 @@ struct Attention {
 __device__ __forceinline__ void seen_by(const Attention& a, int length, int p, int* lo, int* hi) {
   *hi = a.causal && p + 1 < length ? p + 1 : length;
   if (*hi < 0) *hi = 0;
-  *lo = a.window > 0 && p - a.window >= 0 ? p - a.window + 1 : 0;
+  *lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
   if (*lo > *hi) *lo = *hi;
 }
 
