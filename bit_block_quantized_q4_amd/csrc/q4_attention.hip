@@ -20,9 +20,11 @@ namespace {
 // four tiles), and the parts joined in a second launch.
 //
 // Bound by the vector units: some 6 + 2 R instructions for the two codes of a byte, and the
-// LDS reads beside them.  32 heads of 128 on 8 kv heads: one row of 131072 positions 114 us
-// (a workgroup to a row and head, without splits: 4607), 64 sequences of 4096 204 us (468),
-// a prompt of 2000 734 us (2421), 512 rows behind 16384 2.6 ms (9.3).  q of 16 bits, on
+// LDS reads beside them.  They issue in 81% of the busy cycles over one row of 131072
+// positions, in all of them for a prompt of 2000.  32 heads of 128 on 8 kv heads: one row
+// of 131072 positions 121 us, 21 of them the joining of 64 parts by eight workgroups
+// (a workgroup to a row and head, without splits: 4607), 64 sequences of 4096 196 us (468),
+// a prompt of 2000 705 us (2421), 512 rows behind 16384 2.7 ms (9.3).  q of 16 bits, on
 // matrix cores, takes 42, 70, 74 and 203 us.
 template <int NB, int R>
 struct RowLds {
@@ -260,7 +262,9 @@ int64_t row_places(const Attention& a) {
   if (a.batch.offsets == nullptr) return static_cast<int64_t>(a.batch.seqs) * ((a.group + rows - 1) / rows);
   return static_cast<int64_t>(a.batch.tokens) * a.group / rows + a.batch.seqs;
 }
-// Parts of the positions: as many as give each compute unit two workgroups.
+// Parts of the positions: as many as give each compute unit two workgroups, at most 64.
+// (32, 64, 256 of them, one row of one head: 131072 positions 107, 63, 49 us, 1000 positions
+// 15, 18, 40; one row of 32 heads on 8 kv heads, 131072 positions: 184, 122, 122.)
 int row_splits(const Attention& a) {
   const int64_t n = row_places(a) * a.cache.kv_heads, room = 2 * static_cast<int64_t>(device_cu_count());
   return n >= room ? 1 : static_cast<int>(room / n < 64 ? room / n : 64);

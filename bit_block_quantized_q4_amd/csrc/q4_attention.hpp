@@ -22,7 +22,9 @@ constexpr float kLift = 12.f;
 //   above: t = exp(-2 |z|), 1 - 2 t / (1 + t), exp and reciprocal of the hardware (1 ulp).
 // (The second form alone leaves an error of 2^-24 c, which for a c of 10^6 is 0.1.)  Scores
 // of a tile that are all near, as they mostly are, take the polynomial alone: two
-// transcendental instructions less each.
+// transcendental instructions less each.  (6 ragged prompts, 16 heads of 64, window 512: a cap
+// of 50 81 us, as with the second form alone, one of 1, which few scores are near, 115, not 81;
+// without a cap 62.)
 template <bool LOG2>
 struct Cap {
   static constexpr float kNear = 0.625f, kUnit = LOG2 ? kLog2e : 1.f;

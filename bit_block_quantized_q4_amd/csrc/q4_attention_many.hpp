@@ -27,7 +27,8 @@
 // us, not 411.  (q of 32 bits goes another way, with no rounding.)
 //
 // Where there are fewer workgroups than compute units hold the positions are split as
-// well, and the parts joined in a second launch.
+// well, and the parts joined in a second launch; less so beside sequences of few rows, which
+// take places too (many_splits).
 //
 // Bound by issuing vector instructions (taking codes apart, exp, the maximum) beside the
 // matrix products: of 730 us for a prompt of 8000 (40 heads of 128 on 8, bf16) the products
@@ -557,6 +558,14 @@ inline int many_per_unit(int dim) { return dim > 128 ? 1 : dim > 64 ? 2 : 3; }
 // sequences without a tile start workgroups too, of which a quarter more than at once is
 // enough.  (256 rows of each of two sequences behind 16128 positions, heads of 256: whole
 // 955 us, in two parts 509; heads of 128 215 and 174.)
+//
+// At most 32.  What that costs either way, with one kv head (16, 32, 64 parts): 40 rows
+// behind 131072 positions 202, 120, 95 us, behind 8000 29, 30, 40; a prompt of 280 rows and
+// one head of 256, most of whose parts have no positions, 31, 43, 72.
+//
+// A place for every sequence leaves few parts to a chunk beside many of them: 512 rows
+// behind 32488 positions are cut in three alone, 417 us, and not at all beside the next tokens
+// of 64 sequences (106 us alone): 1021 us together.
 inline int many_splits(const Attention& a) {
   const int64_t room = device_cu_count() * static_cast<int64_t>(many_per_unit(a.cache.dim));
   const int64_t rows = static_cast<int64_t>(a.batch.tokens) * a.group;

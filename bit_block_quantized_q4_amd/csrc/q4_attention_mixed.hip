@@ -8,7 +8,11 @@
 namespace q4 {
 namespace {
 
-// Most rows (query rows times heads per kv head) of a sequence of few.
+// Most rows (query rows times heads per kv head) of a sequence of few.  16 sequences within
+// a window of 4096, by this way and by that of many rows: 15 rows 33 and 59 us, 25 rows 44 and
+// 61, 35 rows 59 and 67, 50 rows 61 and 75, 65 rows 78 either way; 64 sequences of 4096, 30
+// rows 90 and 282, 40 rows 160 and 183.  (Up to 64 would be no worse, and some 15% better from
+// 33 on.)
 constexpr int kFewRows = 32;
 
 template <int NB, int NT>

@@ -7,7 +7,8 @@
 // Both only move bytes: reading 401 MB of cache to 1.4 GB of fp16 takes 426 us, 4.3 TB/s
 // (a large copy: 4.65).  Writing 44 MB from 156 MB of bf16 takes 54 us, 3.7 TB/s: the 16
 // codes of a lane are some 300 vector instructions, which at four wavefronts to a SIMD take
-// as long as its bytes do.  Reading that back at once takes 36 us.
+// as long as its bytes do.  Reading that back at once takes 36 us.  (312 MB of fp32 take 94
+// us to write, 3.8 TB/s, and 95 to read back.)
 #include <type_traits>
 
 #include "q4_cache.hpp"
