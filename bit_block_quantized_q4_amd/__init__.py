@@ -913,7 +913,8 @@ def q4_attention(q, cache, tables, lengths, offsets=None, scale=None, causal=Tru
     softcap > 0 bends its scores: softcap * tanh(s / softcap).  Returns y [tokens,
     heads, head_dim] of q's dtype (or y_dtype), with return_lse (y, lse): lse [tokens,
     heads] fp32, the logarithm of the sum of exp.  A row that sees nothing has y 0, lse
-    -inf; rows of no sequence are not written."""
+    -inf, any other with a NaN or an infinity in its q NaN in both; rows of no sequence
+    are not written."""
     if stream is not None:
         with _on(stream, q):
             return q4_attention(q, cache, tables, lengths, offsets, scale, causal, window, softcap, return_lse, y,
